@@ -490,3 +490,6 @@ class CompressedTensor:
         st = torch.full((max(self.t.n_tiles, 1),), 0xFFFF, dtype=torch.int32, device=dev)
         materialize_raw(self.t, sym, w, st, stream)
         return sym, w, st[: self.t.n_tiles]
+
+
+from .mx4 import KV4Cache, MX4Tensor, mx4_quantize  # noqa: E402,F401  (uses the binding above)

@@ -39,7 +39,7 @@ def build(verbose: bool = False) -> str:
     host_o = os.path.join(bdir, "ecw_host.o")
     _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "ecw_host.cpp"), "-o", host_o], verbose)
     objs = [host_o]
-    for src in ("ecw_kernels.hip", "ecw_probes.hip"):
+    for src in ("ecw_kernels.hip", "ecw_probes.hip", "mx4_quant.hip", "mx4_gemm.hip", "kv4.hip"):
         obj = os.path.join(bdir, src.replace(".hip", ".o"))
         _run([HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
         objs.append(obj)

@@ -1,0 +1,797 @@
+// A paged key/value cache in the microscaled 4-bit format: append, read back, attention.
+//
+// Layout of one page of one head (P tokens of D = 32 NB dimensions), all regions
+// whole multiples of 128 bytes:
+//   keys    [P][D / 2]                    a token's codes in order: the matrix
+//                                         instruction's operand for q k^T as it lies
+//   values  [P / 4][16][4][NB]            four tokens x 16 groups of 2 NB dimensions: a
+//                                         lane reads its dimensions of four tokens at once
+//   key scales   [P][NB]
+//   value scales [P / 4][NB][4]
+// Writing a token touches only bytes of its own, so appends never read.
+#include <type_traits>
+
+#include "mx4_common.h"
+
+namespace ecw {
+
+struct Cache {
+  uint8_t* data;
+  uint32_t pages, heads, dim, page_tokens;
+};
+
+// Which rows belong to which sequence and where they stand in it: sequence b's rows
+// are its last tokens.
+struct Batch {
+  const int32_t* table;   // [batch][wide], entries outside 0..pages-1 hold no page
+  const int32_t* lens;    // tokens of each sequence, its new rows among them
+  const int32_t* starts;  // [batch + 1] first rows, or null: rows / batch each
+  int64_t stride;         // of the table
+  uint32_t batch, wide, rows;
+};
+
+inline __host__ __device__ uint64_t region_bytes(const Cache& c) { return (uint64_t)c.page_tokens * c.dim * 17 / 32 * 2; }
+// parts of a region, in bytes
+__device__ __forceinline__ uint32_t plane_bytes(const Cache& c) { return c.page_tokens * (c.dim / 2); }
+__device__ __forceinline__ uint32_t scale_bytes(const Cache& c) { return c.page_tokens * (c.dim / 32); }
+
+// The sequence of a row, its rows and the row's place among them; false: of none.
+__device__ __forceinline__ bool find_row(const Batch& t, uint32_t row, uint32_t* b, int32_t* n, int32_t* i) {
+  if (!t.starts) {
+    const uint32_t each = t.rows / t.batch;
+    *b = row / each;
+    *n = (int32_t)each;
+    *i = (int32_t)(row - *b * each);
+    return true;
+  }
+  uint32_t lo = 0, hi = t.batch;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (t.starts[mid] <= (int32_t)row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int32_t first = t.starts[lo], end = t.starts[lo + 1];
+  *b = lo;
+  *n = end - first;
+  *i = (int32_t)row - first;
+  return first >= 0 && (int32_t)row >= first && (int32_t)row < end;
+}
+
+// The page region of a row's token and the token's place in it; null: it has none.
+__device__ __forceinline__ uint8_t* place(const Cache& c, const Batch& t, uint32_t row, uint32_t head, uint32_t* at) {
+  uint32_t b;
+  int32_t n, i;
+  if (!find_row(t, row, &b, &n, &i)) return nullptr;
+  const int64_t pos = (int64_t)t.lens[b] - n + i;
+  if (pos < 0 || pos >= (int64_t)t.wide * c.page_tokens) return nullptr;
+  const uint32_t p = (uint32_t)((uint64_t)pos / c.page_tokens);
+  const int32_t page = t.table[b * t.stride + p];
+  if (page < 0 || (uint32_t)page >= c.pages) return nullptr;
+  *at = (uint32_t)(pos - (int64_t)p * c.page_tokens);
+  return c.data + ((uint64_t)page * c.heads + head) * region_bytes(c);
+}
+
+// Codes of dimensions 8 u .. 8 u + 7 of a token's value: one word, or for two
+// dimensions a byte (NB = 2: four dimensions a group) two halves.
+__device__ __forceinline__ uint32_t value_at(uint32_t nb, uint32_t token, uint32_t dim) {
+  const uint32_t group = dim / (2 * nb), in = dim % (2 * nb);
+  return ((token / 4 * 16 + group) * 4 + token % 4) * nb + in / 2;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t quantise_row(const void* x, int64_t at, uint32_t u, uint32_t dim, bool vec,
+                                                 uint32_t* byte) {
+  if constexpr (DT == ECW_DT_F32)
+    return quantise_oct(load_oct32(static_cast<const float*>(x) + at, u * 8, dim, vec), byte);
+  else
+    return quantise_oct<DT == ECW_DT_F16>(load_oct16(static_cast<const uint16_t*>(x) + at, u * 8, dim, vec), byte);
+}
+
+// A lane per 8 dimensions of one head of one row, keys and values both.  Bound by
+// memory; for a few rows by the latency of the page look-up and the loads behind it.
+template <int DT>
+__global__ void __launch_bounds__(256) k_kv4_append(Cache c, Batch t, const void* __restrict__ k,
+                                                    const void* __restrict__ v, int64_t k_row, int64_t k_head,
+                                                    int64_t v_row, int64_t v_head, bool k_vec, bool v_vec) {
+  const uint32_t octs = c.dim / 8, nb = c.dim / 32;
+  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t u = (uint32_t)(id % octs);
+  const uint64_t rh = id / octs;
+  const uint32_t row = (uint32_t)(rh / c.heads), head = (uint32_t)(rh - (uint64_t)row * c.heads);
+  if (row >= t.rows) return;  // whole blocks: a head's lanes stay together
+  uint32_t kb, vb, at = 0;
+  const uint32_t kc = quantise_row<DT>(k, row * k_row + head * k_head, u, c.dim, k_vec, &kb);
+  const uint32_t vc = quantise_row<DT>(v, row * v_row + head * v_head, u, c.dim, v_vec, &vb);
+  uint8_t* to = place(c, t, row, head, &at);
+  if (!to) return;
+  *reinterpret_cast<uint32_t*>(to + (uint64_t)at * (c.dim / 2) + u * 4) = kc;
+  uint8_t* vals = to + plane_bytes(c);
+  if (nb == 2) {
+    *reinterpret_cast<uint16_t*>(vals + value_at(2, at, u * 8)) = (uint16_t)vc;
+    *reinterpret_cast<uint16_t*>(vals + value_at(2, at, u * 8 + 4)) = (uint16_t)(vc >> 16);
+  } else {
+    *reinterpret_cast<uint32_t*>(vals + value_at(nb, at, u * 8)) = vc;
+  }
+  if ((u & 3) == 0) {
+    uint8_t* s = to + 2 * plane_bytes(c);
+    s[at * nb + u / 4] = (uint8_t)kb;
+    s[scale_bytes(c) + (at / 4 * nb + u / 4) * 4 + at % 4] = (uint8_t)vb;
+  }
+}
+
+// The values that append's rows stand for, [rows][heads][dim]; zeros where a row has no page.
+template <int DT>
+__global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __restrict__ k, void* __restrict__ v) {
+  const uint32_t octs = c.dim / 8, nb = c.dim / 32;
+  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t u = (uint32_t)(id % octs);
+  const uint64_t rh = id / octs;
+  const uint32_t row = (uint32_t)(rh / c.heads), head = (uint32_t)(rh - (uint64_t)row * c.heads);
+  if (row >= t.rows) return;
+  uint32_t at = 0, kc = 0, vc = 0, kb = kScaleOne, vb = kScaleOne;
+  const uint8_t* from = place(c, t, row, head, &at);
+  if (from) {
+    kc = *reinterpret_cast<const uint32_t*>(from + (uint64_t)at * (c.dim / 2) + u * 4);
+    const uint8_t* vals = from + plane_bytes(c);
+    if (nb == 2)
+      vc = *reinterpret_cast<const uint16_t*>(vals + value_at(2, at, u * 8)) |
+           (uint32_t) * reinterpret_cast<const uint16_t*>(vals + value_at(2, at, u * 8 + 4)) << 16;
+    else
+      vc = *reinterpret_cast<const uint32_t*>(vals + value_at(nb, at, u * 8));
+    const uint8_t* s = from + 2 * plane_bytes(c);
+    kb = s[at * nb + u / 4];
+    vb = s[scale_bytes(c) + (at / 4 * nb + u / 4) * 4 + at % 4];
+  }
+  store_oct<DT>(k, id * 8, kc, scale_of(kb), 8, true);
+  store_oct<DT>(v, id * 8, vc, scale_of(vb), 8, true);
+}
+
+// ------------------------------------------------------------------ attention
+// A wave takes 16 NQ query rows of one sequence and one key/value head (row r: token
+// r / group, query head r % group) and tiles of 32 tokens.  Everything runs
+// transposed, so that no value crosses lanes between the two products: of
+// S^T = K q^T (16x16x32 instructions) lane l gets query l % 16 and tokens
+// 4 (l / 16) .. + 3 of each half tile, which is the operand of O^T += V^T P^T if that
+// instruction's order of tokens is taken the same way; the running maximum, sum and
+// rescaling then belong to the lane's own query column.
+struct AttendArgs {
+  Cache c;
+  Batch t;
+  const uint16_t* q;
+  void* o;
+  float* part;            // per split and row: dim fp32 of O; then per split and row: maximum and sum
+  int64_t q_row, q_head;  // strides
+  uint32_t group, q_heads, q_tiles, splits;
+  int32_t window, sinks;  // window 0: none
+  float scale;            // times log2 e
+  bool vec;
+};
+
+// A row's softmax state: its maximum (in powers of two) and sum.  kNothing as the sum:
+// no token was visible, so the output is zero; a sum of zero from tokens that were
+// visible (all scores -inf) gives NaN, as the definition does.
+constexpr float kNothing = -1.f;
+
+template <int NB>
+struct Tile {  // what a lane holds of 32 tokens
+  uint32_t k[2][NB], v[2][NB];
+  uint32_t ks[2][NB / 4 + 1], vs[2];
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&to)[N], const uint8_t* p) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p + i * 4);
+      to[i] = v[0], to[i + 1] = v[1], to[i + 2] = v[2], to[i + 3] = v[3];
+    }
+  } else {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    to[0] = v[0], to[1] = v[1];
+  }
+}
+
+// value scales of a lane's dimension group: block group * 2 NB / 32
+template <int NB>
+__device__ __forceinline__ void load_tile(Tile<NB>& t, const uint8_t* region, uint32_t page_tokens, uint32_t at,
+                                          uint32_t r16, uint32_t g) {
+  const uint8_t* v = region + page_tokens * (NB * 16);
+  const uint8_t* ks = region + page_tokens * (NB * 32);
+  const uint8_t* vs = ks + page_tokens * NB;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t token = at + 16 * h;
+    load_words<NB>(t.k[h], region + (token + r16) * (NB * 16) + g * (NB * 4));
+    load_words<NB>(t.v[h], v + ((token / 4 + g) * 16 + r16) * (NB * 4));
+    // the lane's NB octets of dimensions g NB .. lie in blocks g NB / 4 ..
+    if constexpr (NB == 8) {
+      const uint32_t two = *reinterpret_cast<const uint16_t*>(ks + (token + r16) * NB + g * 2);
+      t.ks[h][0] = two & 255, t.ks[h][1] = two >> 8;
+    } else {
+      t.ks[h][0] = ks[(token + r16) * NB + g * NB / 4];
+    }
+    t.vs[h] = *reinterpret_cast<const uint32_t*>(vs + ((token / 4 + g) * NB + r16 * NB / 16) * 4);
+  }
+}
+
+__device__ __forceinline__ bool has_nan_scale(uint32_t w) {  // a byte of 255
+  return (((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u) != 0;
+}
+
+// the operand of V^T for dimensions 2 B and 2 B + 1 of the lane's group: byte B of each
+// of the eight tokens, turned from pairs of dimensions into pairs of tokens
+template <int NB, int B>
+__device__ __forceinline__ void value_operands(const Tile<NB>& t, const float (&s)[8], bf16x8* even, bf16x8* odd) {
+  uint32_t p[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (NB == 2) {  // two tokens a word
+      p[4 * h] = pair_bf16<B>(t.v[h][0], s[4 * h]);
+      p[4 * h + 1] = pair_bf16<2 + B>(t.v[h][0], s[4 * h + 1]);
+      p[4 * h + 2] = pair_bf16<B>(t.v[h][1], s[4 * h + 2]);
+      p[4 * h + 3] = pair_bf16<2 + B>(t.v[h][1], s[4 * h + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[4 * h + i] = pair_bf16<B % 4>(t.v[h][i * (NB / 4) + B / 4], s[4 * h + i]);
+    }
+  }
+  u32x4 e, o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x05040100u);
+    o[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x07060302u);
+  }
+  *even = __builtin_bit_cast(bf16x8, e);
+  *odd = __builtin_bit_cast(bf16x8, o);
+}
+
+template <int I, int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<I + 1, N>(f);
+  }
+}
+
+template <int NB, int NQ, bool F16>
+struct Wave {
+  bf16x8 q[NQ][NB], ql[F16 ? NQ : 1][F16 ? NB : 1];
+  int32_t pos[NQ];  // of the lane's query row in each tile, -1: no row
+  f32x4 o[NQ][2 * NB];
+  float m[NQ], l[NQ];
+  bool seen[NQ];
+
+  __device__ __forceinline__ bool visible(const AttendArgs& a, int32_t t, int32_t p) const {
+    return t <= p && (a.window == 0 || t > p - a.window || t < a.sinks);
+  }
+
+  // One tile of tokens from t0 on; whole: every row sees every token.
+  __device__ __forceinline__ void tile(const AttendArgs& a, Tile<NB>& t, int32_t t0, bool whole, int32_t stored,
+                                       uint32_t g) {
+    f32x4 s[2][NQ];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const bf16x8 k = oct_bf16(t.k[h][j], scale_of(t.ks[h][j / 4]));
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          s[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[n][j], s[h][n], 0, 0, 0);
+          if constexpr (F16) s[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, ql[n][j], s[h][n], 0, 0, 0);
+        }
+      }
+    }
+    // tokens past the last one stored hold anything: as zeros they add nothing
+    if (t0 + 32 > stored) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t0 + 16 * h + 4 * (int32_t)g + i >= stored) clear_value(t, h, i);
+    }
+    bf16x8 p[NQ];
+    uint32_t vis[NQ];  // bits: the lane's eight tokens
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float x[8], top = -INFINITY;
+      vis[n] = 0xff;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = s[i / 4][n][i % 4] * a.scale;
+      if (!whole) {
+        vis[n] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (visible(a, t0 + 16 * (i / 4) + 4 * (int32_t)g + i % 4, pos[n])) vis[n] |= 1u << i;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!(vis[n] >> i & 1)) x[i] = -INFINITY;
+      }
+      seen[n] |= vis[n] != 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float now = fmaxf(m[n], top), base = now == -INFINITY ? 0.f : now;
+      const float fade = __builtin_amdgcn_exp2f(m[n] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(x[i] - base);
+        sum += x[i];
+      }
+      // the weights are rounded to bf16, 2^-9 of each, for the second product; their sum is not
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[n][i] = (__bf16)x[i];
+      l[n] = l[n] * fade + sum;
+      if (__any(now != m[n])) {
+#pragma unroll
+        for (int d = 0; d < 2 * NB; ++d) o[n][d] *= fade;
+      }
+      m[n] = now;
+    }
+    if (__any(has_nan_scale(t.vs[0]) || has_nan_scale(t.vs[1]))) mark_nan(t, vis);
+    float vs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) vs[i] = scale_of(t.vs[i / 4] >> 8 * (i % 4) & 255);
+    each<0, NB>([&](auto b) {
+      bf16x8 even, odd;
+      value_operands<NB, b.value>(t, vs, &even, &odd);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        o[n][2 * b.value] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, p[n], o[n][2 * b.value], 0, 0, 0);
+        o[n][2 * b.value + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, p[n], o[n][2 * b.value + 1], 0, 0, 0);
+      }
+    });
+  }
+
+  // A token's value as zeros of scale 1; i: the token among the lane's four of half h.
+  __device__ __forceinline__ void clear_value(Tile<NB>& t, int h, int i) const {
+    if constexpr (NB == 2) {
+      t.v[h][i / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
+    } else {
+#pragma unroll
+      for (int w = 0; w < NB / 4; ++w) t.v[h][i * (NB / 4) + w] = 0;
+    }
+    t.vs[h] = (t.vs[h] & ~(255u << 8 * i)) | kScaleOne << 8 * i;
+  }
+
+  // Value blocks that are NaN: a weight of zero times NaN must not reach rows that do not
+  // see the token, so these blocks count as zeros, and the rows that see one become NaN
+  // in its dimensions.  A product of ones marks them.
+  __device__ __forceinline__ void mark_nan(Tile<NB>& t, const uint32_t (&vis)[NQ]) {
+    u32x4 is{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((t.vs[i / 4] >> 8 * (i % 4) & 255) != kScaleNaN) continue;
+      is[i / 2] |= 0x3f80u << 16 * (i % 2);
+      clear_value(t, i / 4, i % 4);
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      u32x4 see{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (vis[n] >> i & 1) see[i / 2] |= 0x3f80u << 16 * (i % 2);
+      const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, is),
+                                                                __builtin_bit_cast(bf16x8, see),
+                                                                f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+      for (int d = 0; d < 2 * NB; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (hit[r] > 0.f) o[n][d][r] = __builtin_nanf("");
+    }
+  }
+};
+
+// Zeros for the rows before the first sequence's and behind the last one's.
+template <int D>
+__device__ void none(const AttendArgs& a) {
+  if (blockIdx.y != 0) return;
+  const uint32_t lo = (uint32_t)min(max(a.t.starts[0], 0), (int32_t)a.t.rows);
+  const uint32_t hi = min((uint32_t)max(a.t.starts[a.t.batch], (int32_t)lo), a.t.rows);
+  const uint64_t all = (uint64_t)a.t.rows * a.q_heads, before = (uint64_t)lo * a.q_heads;
+  const uint64_t nobody = before + (uint64_t)(a.t.rows - hi) * a.q_heads;
+  for (uint64_t e = threadIdx.x; e < nobody; e += 256) {
+    const uint64_t at = e < before ? e : e - before + (uint64_t)hi * a.q_heads;
+    if (a.splits > 1) {
+      a.part[a.splits * all * D + (blockIdx.x * all + at) * 2 + 1] = kNothing;
+    } else {
+      for (int d = 0; d < D; ++d) static_cast<uint16_t*>(a.o)[at * D + d] = 0;
+    }
+  }
+}
+
+// A row's output: element e of NB * 2 tiles x 4 of the lane is dimension
+// 2 NB (4 g + e % 4) + e / 4.
+template <int NB, int NQ, bool F16>
+__global__ void __launch_bounds__(256) k_kv4_attend(AttendArgs a) {
+  constexpr int D = 32 * NB;
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t r16 = lane & 15, g = lane >> 4;
+  const uint32_t b = blockIdx.z, head = blockIdx.y % a.c.heads, q_tile = blockIdx.y / a.c.heads;
+  if (b == a.t.batch) {  // rows of no sequence
+    none<D>(a);
+    return;
+  }
+  int32_t first = 0, n_rows = (int32_t)(a.t.rows / a.t.batch);
+  if (a.t.starts) {
+    first = max(a.t.starts[b], 0);
+    n_rows = max(min(a.t.starts[b + 1], (int32_t)a.t.rows), 0) - first;
+  } else {
+    first = (int32_t)b * n_rows;
+  }
+  const int64_t all_rows = (int64_t)max(n_rows, 0) * a.group;
+  const int32_t len = a.t.lens[b];
+  __shared__ float sm[4][16 * NQ], sl[4][16 * NQ];
+  __shared__ float so[4][16][D + 4];
+  for (int64_t row0 = (int64_t)q_tile * (16 * NQ); row0 < all_rows; row0 += (int64_t)a.q_tiles * (16 * NQ)) {
+  const int64_t capacity = (int64_t)a.t.wide * a.c.page_tokens;
+  // positions of the tile's first and last rows
+  const int64_t last_row = min(row0 + 16 * NQ, all_rows) - 1;
+  const int64_t p_lo = (int64_t)len - n_rows + row0 / a.group, p_hi = (int64_t)len - n_rows + last_row / a.group;
+  const int64_t hi = min(p_hi, capacity - 1);
+  // tiles: those of the sinks, then from the window's first on
+  int32_t first_tile = 0, sink_tiles = 0, tiles = 0;
+  if (hi >= 0) {
+    if (a.window) first_tile = (int32_t)(max(p_lo - a.window + 1, (int64_t)0) / 32);
+    sink_tiles = min(min((a.sinks + 31) / 32, first_tile), (int32_t)(hi / 32) + 1);
+    tiles = max((int32_t)(hi / 32) - first_tile + 1, 0) + sink_tiles;
+  }
+  const uint32_t parts = a.splits * 4, part = blockIdx.x * 4 + wave;
+  const int32_t from = (int32_t)((int64_t)tiles * part / parts), to = (int32_t)((int64_t)tiles * (part + 1) / parts);
+
+  Wave<NB, NQ, F16> w;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int64_t r = min(row0 + n * 16 + r16, all_rows - 1);
+    const uint32_t i = (uint32_t)(r / a.group), hq = head * a.group + (uint32_t)(r - (int64_t)i * a.group);
+    w.pos[n] = row0 + n * 16 + r16 < all_rows ? (int32_t)max((int64_t)len - n_rows + i, (int64_t)-1) : -1;
+    const uint16_t* q = a.q + (first + (int64_t)i) * a.q_row + hq * a.q_head;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const u32x4 v = load_oct16(q, (g * NB + j) * 8, D, a.vec).v;
+      if constexpr (F16)
+        split_f16(v, &w.q[n][j], &w.ql[n][j]);
+      else
+        w.q[n][j] = __builtin_bit_cast(bf16x8, v);
+    }
+    w.m[n] = -INFINITY;
+    w.l[n] = 0.f;
+    w.seen[n] = false;
+#pragma unroll
+    for (int d = 0; d < 2 * NB; ++d) w.o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int32_t* table = a.t.table + b * a.t.stride;
+  for (int32_t v = from; v < to; ++v) {
+    const int32_t t0 = (v < sink_tiles ? v : v - sink_tiles + first_tile) * 32;
+    const uint32_t in_table = (uint32_t)t0 / a.c.page_tokens;
+    const int32_t page = table[in_table];
+    if (page < 0 || (uint32_t)page >= a.c.pages) continue;
+    Tile<NB> t;
+    load_tile<NB>(t, a.c.data + ((uint64_t)page * a.c.heads + head) * region_bytes(a.c), a.c.page_tokens,
+                  (uint32_t)t0 - in_table * a.c.page_tokens, r16, g);
+    const bool whole = t0 + 31 <= p_lo && row0 + 16 * NQ <= all_rows &&
+                       (a.window == 0 || t0 > p_hi - a.window || t0 + 32 <= a.sinks);
+    w.tile(a, t, t0, whole, (int32_t)min((int64_t)len, capacity), g);
+  }
+
+  // the four waves' states joined through LDS
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    float l = w.l[n];
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    uint32_t seen = w.seen[n];
+    seen |= (uint32_t)__shfl_xor((int)seen, 16);
+    seen |= (uint32_t)__shfl_xor((int)seen, 32);
+    if (g == 0) {
+      sm[wave][n * 16 + r16] = w.m[n];
+      sl[wave][n * 16 + r16] = seen ? l : kNothing;
+    }
+  }
+  const uint64_t all = (uint64_t)a.t.rows * a.q_heads;
+  for (int n = 0; n < NQ; ++n) {
+    __syncthreads();
+#pragma unroll
+    for (int nn = 0; nn < NQ; ++nn)
+      if (nn == n) {
+#pragma unroll
+        for (int d = 0; d < 2 * NB; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) so[wave][r16][2 * NB * (4 * g + r) + d] = w.o[nn][d][r];
+      }
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < 16 * D; e += 256) {
+      const uint32_t row = e / D, d = e % D;
+      const int64_t r = row0 + n * 16 + row;
+      if (r >= all_rows) continue;
+      float m = -INFINITY, l = 0.f, o = 0.f;
+      bool seen = false;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (sl[v][n * 16 + row] == kNothing) continue;
+        seen = true;
+        m = fmaxf(m, sm[v][n * 16 + row]);
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (sl[v][n * 16 + row] == kNothing) continue;
+        const float f = __builtin_amdgcn_exp2f(sm[v][n * 16 + row] - base);
+        l += f * sl[v][n * 16 + row];
+        o += f * so[v][row][d];
+      }
+      const uint32_t i = (uint32_t)(r / a.group);
+      const uint64_t at = (first + (uint64_t)i) * a.q_heads + head * a.group + (uint32_t)(r - (int64_t)i * a.group);
+      if (a.splits == 1) {
+        const float y = seen ? o / l : 0.f;
+        if constexpr (F16)
+          static_cast<_Float16*>(a.o)[at * D + d] = (_Float16)y;
+        else
+          static_cast<__bf16*>(a.o)[at * D + d] = (__bf16)y;
+      } else {
+        a.part[(blockIdx.x * all + at) * D + d] = o;
+        if (d == 0) {
+          float* ml = a.part + a.splits * all * D + (blockIdx.x * all + at) * 2;
+          ml[0] = m;
+          ml[1] = seen ? l : kNothing;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  }
+}
+
+// The splits of a row joined, in their order.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) k_kv4_join(const float* __restrict__ part, void* __restrict__ out, uint64_t all,
+                                                  uint32_t splits) {
+  const uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x, at = e / D;
+  if (at >= all) return;
+  const float* ml = part + splits * all * D;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  bool seen = false;
+  for (uint32_t s = 0; s < splits; ++s) {
+    if (ml[(s * all + at) * 2 + 1] == kNothing) continue;
+    seen = true;
+    m = fmaxf(m, ml[(s * all + at) * 2]);
+  }
+  const float base = m == -INFINITY ? 0.f : m;
+  for (uint32_t s = 0; s < splits; ++s) {
+    const float ls = ml[(s * all + at) * 2 + 1];
+    if (ls == kNothing) continue;
+    const float f = __builtin_amdgcn_exp2f(ml[(s * all + at) * 2] - base);
+    l += f * ls;
+    o += f * part[s * all * D + e];
+  }
+  const float y = seen ? o / l : 0.f;
+  if constexpr (F16)
+    static_cast<_Float16*>(out)[e] = (_Float16)y;
+  else
+    static_cast<__bf16*>(out)[e] = (__bf16)y;
+}
+
+
+}  // namespace ecw
+
+using namespace ecw;
+
+namespace {
+
+ecw_status check_cache(const ecw_kv4* c) {
+  if (!c) return refuse(ECW_E_INVALID_ARG, "cache is NULL");
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return refuse(ECW_E_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+  if (c->page_tokens == 0 || c->page_tokens % 32 || c->page_tokens > 4096)
+    return refuse(ECW_E_INVALID_ARG, "page_tokens must be a multiple of 32 up to 4096");
+  if (c->pages == 0 || c->pages >= 1u << 31 || c->kv_heads == 0 || c->kv_heads > 1024)
+    return refuse(ECW_E_INVALID_ARG, "pages must be in [1, 2^31), kv_heads in [1, 1024]");
+  return ECW_OK;
+}
+
+ecw_status check_rows(const ecw_kv4* c, const ecw_kv4_rows* r) {
+  if (ecw_status s = check_cache(c)) return s;
+  if (!c->data || !aligned(c->data, 256)) return refuse(ECW_E_INVALID_ARG, "cache data must be 256-byte aligned");
+  if (!r) return refuse(ECW_E_INVALID_ARG, "rows are NULL");
+  if (r->rows == 0) return ECW_OK;
+  if (r->batch == 0 || r->batch > 65534 || r->rows >= 1u << 30)
+    return refuse(ECW_E_INVALID_ARG, "batch must be in [1, 65534], rows below 2^30");
+  if (!r->starts && r->rows % r->batch)
+    return refuse(ECW_E_INVALID_ARG, "without starts every sequence has the same number of rows");
+  if (!r->lens || (r->table_width && !r->page_table)) return refuse(ECW_E_INVALID_ARG, "lens or page table is NULL");
+  if (!aligned(r->lens, 4) || !aligned(r->page_table, 4) || !aligned(r->starts, 4))
+    return refuse(ECW_E_INVALID_ARG, "lens, page table and starts must be 4-byte aligned");
+  if (r->table_stride < 0) return refuse(ECW_E_INVALID_ARG, "table stride must not be negative");
+  if ((uint64_t)r->table_width * c->page_tokens >= 1u << 30)
+    return refuse(ECW_E_INVALID_ARG, "the page table spans 2^30 tokens or more");
+  return ECW_OK;
+}
+
+Cache cache_of(const ecw_kv4* c) {
+  return {static_cast<uint8_t*>(c->data), c->pages, c->kv_heads, c->head_dim, c->page_tokens};
+}
+Batch batch_of(const ecw_kv4_rows* r) {
+  return {r->page_table, r->lens, r->starts, r->table_stride, r->batch, r->table_width, r->rows};
+}
+
+bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
+  const uint64_t n = ((uint64_t)r->rows * c->kv_heads * (c->head_dim / 8) + 255) / 256;
+  *grid = (uint32_t)n;
+  return n >> 31 == 0;
+}
+
+// How an attention call is cut up: query tiles of 16 nq rows, and splits of each
+// sequence's tokens.
+struct Plan {
+  uint32_t nq, q_tiles, splits;
+};
+
+Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
+  Plan p;
+  const uint64_t group = at->q_heads / c->kv_heads;
+  const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;
+  const uint64_t rows = each * group;
+  p.nq = rows <= 16 ? 1 : 2;
+  uint64_t tiles_q = (rows + 16 * p.nq - 1) / (16 * p.nq);
+  const uint64_t most = 65535 / c->kv_heads;
+  p.q_tiles = (uint32_t)(tiles_q < most ? tiles_q : most);
+  uint64_t len = (uint64_t)r->table_width * c->page_tokens;
+  if (at->max_len && at->max_len < len) len = at->max_len;
+  if (at->window) {
+    const uint64_t seen = (uint64_t)at->window + at->sinks + each;
+    if (seen < len) len = seen;
+  }
+  const uint64_t tiles = (len + 31) / 32, blocks = (uint64_t)p.q_tiles * c->kv_heads * r->batch;
+  uint64_t splits = (1024 + blocks - 1) / blocks;
+  const uint64_t top = (tiles + 7) / 8;  // two tiles a wave at least
+  if (splits > top) splits = top;
+  if (splits > 64) splits = 64;
+  p.splits = splits ? (uint32_t)splits : 1;
+  return p;
+}
+
+ecw_status check_attention(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
+  if (ecw_status s = check_rows(c, r)) return s;
+  if (!at) return refuse(ECW_E_INVALID_ARG, "attention is NULL");
+  if (at->q_heads == 0 || at->q_heads % c->kv_heads || at->q_heads > 65536)
+    return refuse(ECW_E_INVALID_ARG, "q_heads must be a positive multiple of kv_heads, at most 65536");
+  if (at->window > 1u << 30 || at->sinks > 1u << 30)
+    return refuse(ECW_E_INVALID_ARG, "window and sinks must be at most 2^30");
+  if (!(at->scale - at->scale == 0.f)) return refuse(ECW_E_INVALID_ARG, "scale must be finite");
+  return ECW_OK;
+}
+
+uint64_t part_bytes(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at, const Plan& p) {
+  return p.splits == 1 ? 0 : (uint64_t)p.splits * r->rows * at->q_heads * (c->head_dim + 2) * 4;
+}
+
+template <int NB, int NQ, bool F16>
+void launch_attend(hipStream_t stream, const AttendArgs& a) {
+  const uint32_t z = a.t.batch + (a.t.starts ? 1 : 0);
+  hipLaunchKernelGGL((k_kv4_attend<NB, NQ, F16>), dim3(a.splits, a.q_tiles * a.c.heads, z), dim3(256), 0, stream, a);
+}
+
+template <int NB, bool F16>
+ecw_status launch_all(hipStream_t stream, const AttendArgs& a, uint32_t nq) {
+  if (nq == 1)
+    launch_attend<NB, 1, F16>(stream, a);
+  else
+    launch_attend<NB, 2, F16>(stream, a);
+  if (ecw_status s = launched("kv4_attend")) return s;
+  if (a.splits == 1) return ECW_OK;
+  const uint64_t all = (uint64_t)a.t.rows * a.q_heads, grid = (all * (32 * NB) + 255) / 256;
+  hipLaunchKernelGGL((k_kv4_join<32 * NB, F16>), dim3((uint32_t)grid), dim3(256), 0, stream, a.part, a.o, all,
+                     a.splits);
+  return launched("kv4_attend");
+}
+
+template <bool F16>
+ecw_status launch_dim(hipStream_t stream, const AttendArgs& a, uint32_t nq) {
+  switch (a.c.dim) {
+    case 64: return launch_all<2, F16>(stream, a, nq);
+    case 128: return launch_all<4, F16>(stream, a, nq);
+    default: return launch_all<8, F16>(stream, a, nq);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+ecw_status kv4_bytes(const ecw_kv4* cache, size_t* bytes) {
+  if (ecw_status s = check_cache(cache)) return s;
+  if (!bytes) return refuse(ECW_E_INVALID_ARG, "bytes is NULL");
+  *bytes = (size_t)cache->pages * cache->kv_heads * region_bytes(cache_of(cache));
+  return ECW_OK;
+}
+
+ecw_status kv4_append(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, const void* k, const void* v,
+                      int dtype, const int64_t* strides) {
+  if (ecw_status s = check_rows(cache, rows)) return s;
+  if (dtype != ECW_DT_F16 && dtype != ECW_DT_BF16 && dtype != ECW_DT_F32)
+    return refuse(ECW_E_INVALID_ARG, "k and v must be F16, BF16 or F32");
+  if (rows->rows == 0) return ECW_OK;
+  const int64_t size = dtype == ECW_DT_F32 ? 4 : 2;
+  if (!k || !v || !strides || !aligned(k, size) || !aligned(v, size))
+    return refuse(ECW_E_INVALID_ARG, "k and v must be aligned device pointers with strides");
+  for (int i = 0; i < 4; ++i)
+    if (strides[i] < 0) return refuse(ECW_E_INVALID_ARG, "strides must not be negative");
+  uint32_t grid;
+  if (!row_grid(cache, rows, &grid)) return refuse(ECW_E_UNSUPPORTED, "too many rows for one launch");
+  const bool kv = aligned(k, 16) && strides[0] * size % 16 == 0 && strides[1] * size % 16 == 0;
+  const bool vv = aligned(v, 16) && strides[2] * size % 16 == 0 && strides[3] * size % 16 == 0;
+  auto* fn = dtype == ECW_DT_F32   ? k_kv4_append<ECW_DT_F32>
+             : dtype == ECW_DT_F16 ? k_kv4_append<ECW_DT_F16>
+                                   : k_kv4_append<ECW_DT_BF16>;
+  hipLaunchKernelGGL(fn, dim3(grid), dim3(256), 0, (hipStream_t)stream, cache_of(cache), batch_of(rows), k, v,
+                     strides[0], strides[1], strides[2], strides[3], kv, vv);
+  return launched("kv4_append");
+}
+
+ecw_status kv4_read(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, void* k, void* v, int dtype) {
+  if (ecw_status s = check_rows(cache, rows)) return s;
+  if (dtype != ECW_DT_F16 && dtype != ECW_DT_BF16 && dtype != ECW_DT_F32)
+    return refuse(ECW_E_INVALID_ARG, "k and v must be F16, BF16 or F32");
+  if (rows->rows == 0) return ECW_OK;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16))
+    return refuse(ECW_E_INVALID_ARG, "k and v must be 16-byte aligned device pointers");
+  uint32_t grid;
+  if (!row_grid(cache, rows, &grid)) return refuse(ECW_E_UNSUPPORTED, "too many rows for one launch");
+  auto* fn = dtype == ECW_DT_F32   ? k_kv4_read<ECW_DT_F32>
+             : dtype == ECW_DT_F16 ? k_kv4_read<ECW_DT_F16>
+                                   : k_kv4_read<ECW_DT_BF16>;
+  hipLaunchKernelGGL(fn, dim3(grid), dim3(256), 0, (hipStream_t)stream, cache_of(cache), batch_of(rows), k, v);
+  return launched("kv4_read");
+}
+
+ecw_status kv4_attend_workspace_size(const ecw_kv4* cache, const ecw_kv4_rows* rows, const ecw_kv4_attention* at,
+                                     size_t* bytes) {
+  if (ecw_status s = check_attention(cache, rows, at)) return s;
+  if (!bytes) return refuse(ECW_E_INVALID_ARG, "bytes is NULL");
+  *bytes = rows->rows ? (size_t)part_bytes(cache, rows, at, plan_of(cache, rows, at)) : 0;
+  return ECW_OK;
+}
+
+ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, const ecw_kv4_attention* at,
+                      const void* q, int dtype, int64_t q_row, int64_t q_head, void* o, void* workspace,
+                      size_t workspace_bytes) {
+  if (ecw_status s = check_attention(cache, rows, at)) return s;
+  if (dtype != ECW_DT_F16 && dtype != ECW_DT_BF16) return refuse(ECW_E_INVALID_ARG, "q must be F16 or BF16");
+  if (rows->rows == 0) return ECW_OK;
+  if (!q || !aligned(q, 2) || q_row < 0 || q_head < 0)
+    return refuse(ECW_E_INVALID_ARG, "q must be an aligned device pointer with strides of 0 or more");
+  if (!o || !aligned(o, 16)) return refuse(ECW_E_INVALID_ARG, "o must be a 16-byte aligned device pointer");
+  const Plan p = plan_of(cache, rows, at);
+  if (part_bytes(cache, rows, at, p) > workspace_bytes || (p.splits > 1 && (!workspace || !aligned(workspace, 16))))
+    return refuse(ECW_E_INVALID_ARG, "workspace missing, too small or not 16-byte aligned");
+  if (((uint64_t)rows->rows * at->q_heads * cache->head_dim + 255) / 256 >> 31)
+    return refuse(ECW_E_UNSUPPORTED, "too many rows for one launch");
+  AttendArgs a{};
+  a.c = cache_of(cache);
+  a.t = batch_of(rows);
+  a.q = static_cast<const uint16_t*>(q);
+  a.o = o;
+  a.part = static_cast<float*>(workspace);
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.group = at->q_heads / cache->kv_heads;
+  a.q_heads = at->q_heads;
+  a.q_tiles = p.q_tiles;
+  a.splits = p.splits;
+  a.window = (int32_t)at->window;
+  a.sinks = (int32_t)at->sinks;
+  a.scale = at->scale * 1.44269504088896f;
+  a.vec = aligned(q, 16) && q_row % 8 == 0 && q_head % 8 == 0;
+  return dtype == ECW_DT_F16 ? launch_dim<true>((hipStream_t)stream, a, p.nq)
+                             : launch_dim<false>((hipStream_t)stream, a, p.nq);
+}
+
+}  // extern "C"

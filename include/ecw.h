@@ -361,6 +361,84 @@ ecw_status dec_dequantize(ecw_stream stream, const ecw_tensor* t, void* w_out, i
 const char* ecw_last_error(void);
 uint32_t ecw_abi_version(void);
 
+/*
+ * The microscaled 4-bit format (MX4): matrices and a key/value cache at a fixed 4.25
+ * bits per element, next to the entropy-coded weights above.
+ *
+ * 32 neighbouring elements of a row (or of a head) share a scale 2^s, stored as the
+ * byte s + 127; an element is one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 or a negative of them
+ * times the scale, in 4 bits, the lower element in the lower half of a byte.
+ *   s = floor(log2(largest magnitude)) - 2, held to -125..125 (an all-zero block: 0)
+ *   elements round to nearest, ties to the even code; magnitudes over 6 become 6
+ * A block with an infinity or a NaN has the byte 255 and stands for NaN.  Zeros past
+ * the last column fill a row up to a multiple of 128 columns.
+ *   codes  [rows][ceil(cols / 128) * 64] bytes     scales [rows][ceil(cols / 128) * 4] bytes
+ * both 16-byte aligned device memory.  No call needs zero-filled or persistent
+ * workspace; calls with rows or batch of zero launch nothing.
+ */
+
+/* x [rows][cols] fp16, bf16 or fp32, row_stride elements apart -> codes, scales. */
+ecw_status mx4_quantize(ecw_stream stream, const void* x, int x_dtype, int64_t row_stride, uint32_t rows,
+                        uint32_t cols, void* codes, void* scales);
+/* The values as a dense [rows][cols] matrix: exact in fp32 and bf16, rounded to nearest
+ * even in fp16 (infinite past its range). */
+ecw_status mx4_dequantize(ecw_stream stream, const void* codes, const void* scales, uint32_t rows, uint32_t cols,
+                          void* out, int out_dtype);
+/* y [batch][rows] (fp32, fp16 or bf16) = x w^T, x [batch][cols] fp16 or bf16, rows
+ * x_stride elements apart; products exact, sums in fp32, one rounding into y. */
+ecw_status mx4_gemm(ecw_stream stream, const void* w_codes, const void* w_scales, uint32_t rows, uint32_t cols,
+                    const void* x, int x_dtype, int64_t x_stride, uint32_t batch, void* y, int y_dtype);
+/* The same with x in the 4-bit format too. */
+ecw_status mx4_gemm_mx4(ecw_stream stream, const void* w_codes, const void* w_scales, uint32_t rows, uint32_t cols,
+                        const void* x_codes, const void* x_scales, uint32_t batch, void* y, int y_dtype);
+
+/* A paged key/value cache in the 4-bit format.  Pages hold page_tokens tokens of every
+ * head; their inner layout is the library's. */
+typedef struct {
+  void* data;            /* kv4_bytes() bytes of device memory, 256-byte aligned */
+  uint32_t pages;
+  uint32_t kv_heads;
+  uint32_t head_dim;     /* 64, 128 or 256 */
+  uint32_t page_tokens;  /* a multiple of 32 */
+} ecw_kv4;
+
+/* Rows of a call and where they stand.  Row r of sequence b is one of its last tokens:
+ * with n rows, row i is token lens[b] - n + i.  An entry of the page table outside
+ * 0..pages-1 is no page: nothing is written to it and its tokens are not visible.  All
+ * arrays are device memory and their values are checked on the device, never trusted. */
+typedef struct {
+  const int32_t* page_table; /* [batch][table_width], rows table_stride apart */
+  int64_t table_stride;
+  const int32_t* lens;       /* [batch] tokens of each sequence, the call's rows among them */
+  const int32_t* starts;     /* [batch + 1] first rows, ascending; NULL: rows / batch each */
+  uint32_t batch, table_width, rows;
+} ecw_kv4_rows;
+
+typedef struct {
+  uint32_t q_heads;          /* a multiple of kv_heads: query head h reads head h / (q_heads / kv_heads) */
+  uint32_t max_rows;         /* most rows of one sequence, 0 unknown: for the launch's shape only */
+  uint32_t max_len;          /* most tokens of one sequence, 0 unknown: for the launch's shape only */
+  uint32_t window;           /* a row sees its last `window` tokens, its own among them; 0: all */
+  uint32_t sinks;            /* and, with a window, the first `sinks` tokens */
+  float scale;               /* of the scores */
+} ecw_kv4_attention;
+
+ecw_status kv4_bytes(const ecw_kv4* cache, size_t* bytes);
+/* k, v [rows][kv_heads][head_dim] fp16, bf16 or fp32 into the cache; strides: of k's
+ * rows and heads, then of v's, in elements. */
+ecw_status kv4_append(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, const void* k, const void* v,
+                      int dtype, const int64_t* strides);
+/* The values of the same rows out of the cache, dense; zeros for a row without a page. */
+ecw_status kv4_read(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, void* k, void* v, int dtype);
+/* o [rows][q_heads][head_dim] = softmax(scale q k^T) v over the visible tokens, causal
+ * inside a sequence's rows; q and o fp16 or bf16, q's strides in elements.  A row that
+ * sees nothing gives zeros.  The workspace need not be cleared. */
+ecw_status kv4_attend_workspace_size(const ecw_kv4* cache, const ecw_kv4_rows* rows, const ecw_kv4_attention* at,
+                                     size_t* bytes);
+ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, const ecw_kv4_attention* at,
+                      const void* q, int dtype, int64_t q_row, int64_t q_head, void* o, void* workspace,
+                      size_t workspace_bytes);
+
 #ifdef __cplusplus
 }
 #endif

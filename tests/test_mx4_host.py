@@ -1,0 +1,141 @@
+"""Refusals of the 4-bit entry points, through the C ABI and without a GPU: a bad call
+returns its status before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import entropy_coded_weight_amd as ecw
+from entropy_coded_weight_amd import mx4
+
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+P = 1 << 20  # an aligned address that nothing reads
+
+
+@pytest.fixture(scope="module")
+def L():
+    return mx4._lib()
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"rows": 0}, OK), ({"cols": 0}, INVALID), ({"codes": 0}, INVALID), ({"codes": P + 8}, INVALID),
+    ({"scales": P + 4}, INVALID), ({"x": 0}, INVALID), ({"x": P + 1}, INVALID), ({"dtype": ecw.DT_I8}, INVALID),
+    ({"stride": -1}, INVALID), ({"rows": 1 << 31}, INVALID), ({"cols": 1 << 31}, INVALID),
+    ({"rows": 1 << 30, "cols": 1 << 30}, INVALID), ({"rows": 1 << 28, "cols": 1 << 14}, UNSUPPORTED)])
+def test_quantize_and_dequantize(L, change, status):
+    a = {"x": P, "dtype": ecw.DT_BF16, "stride": 64, "rows": 2, "cols": 64, "codes": P, "scales": P, **change}
+    assert L.mx4_quantize(None, a["x"], a["dtype"], a["stride"], a["rows"], a["cols"], a["codes"], a["scales"]) == status
+    if "stride" not in change:
+        assert L.mx4_dequantize(None, a["codes"], a["scales"], a["rows"], a["cols"], a["x"], a["dtype"]) == status
+    if status:
+        assert L.ecw_last_error()
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"batch": 0}, OK), ({"rows": 0}, OK), ({"cols": 0}, INVALID), ({"w": P + 8}, INVALID), ({"ws": 0}, INVALID),
+    ({"x": 0}, INVALID), ({"x": P + 1}, INVALID), ({"y": 0}, INVALID), ({"y": P + 8}, INVALID),
+    ({"xd": ecw.DT_F32}, INVALID), ({"yd": ecw.DT_I8}, INVALID), ({"stride": -8}, INVALID),
+    ({"batch": 1 << 25}, INVALID), ({"rows": 1 << 31}, INVALID)])
+def test_gemm(L, change, status):
+    a = {"w": P, "ws": P, "rows": 16, "cols": 64, "x": P, "xd": ecw.DT_F16, "stride": 64, "batch": 2, "y": P,
+         "yd": ecw.DT_F32, **change}
+    assert L.mx4_gemm(None, a["w"], a["ws"], a["rows"], a["cols"], a["x"], a["xd"], a["stride"], a["batch"], a["y"],
+                      a["yd"]) == status
+    if not {"xd", "stride"} & set(change):
+        assert L.mx4_gemm_mx4(None, a["w"], a["ws"], a["rows"], a["cols"], a["x"], a["x"], a["batch"], a["y"],
+                              a["yd"]) == status
+
+
+CACHES = [({"head_dim": 96}, UNSUPPORTED), ({"page_tokens": 0}, INVALID), ({"page_tokens": 40}, INVALID),
+          ({"page_tokens": 8192}, INVALID), ({"pages": 0}, INVALID), ({"kv_heads": 0}, INVALID),
+          ({"kv_heads": 2000}, INVALID)]
+ROWS = [({"data": 0}, INVALID), ({"data": P + 16}, INVALID), ({"rows": 0}, OK), ({"batch": 0}, INVALID),
+        ({"batch": 70000}, INVALID), ({"rows": 5}, INVALID), ({"rows": 1 << 30}, INVALID), ({"lens": 0}, INVALID),
+        ({"lens": P + 2}, INVALID), ({"page_table": 0}, INVALID), ({"page_table": P + 1}, INVALID),
+        ({"starts": P + 2}, INVALID), ({"table_stride": -1}, INVALID), ({"table_width": 1 << 26}, INVALID)]
+TIMES = [({"q_heads": 0}, INVALID), ({"q_heads": 3}, INVALID), ({"window": 1 << 31}, INVALID),
+         ({"sinks": 1 << 31}, INVALID), ({"scale": float("inf")}, INVALID), ({"scale": float("nan")}, INVALID)]
+
+
+def _cache(change):
+    a = {"data": P, "pages": 4, "kv_heads": 2, "head_dim": 64, "page_tokens": 64}
+    a.update({k: v for k, v in change.items() if k in a})
+    return mx4._Cache(*a.values())
+
+
+def _rows(change):
+    a = {"page_table": P, "table_stride": 4, "lens": P, "starts": 0, "batch": 2, "table_width": 4, "rows": 2}
+    a.update({k: v for k, v in change.items() if k in a})
+    return mx4._Rows(*a.values())
+
+
+def _attention(change):
+    a = {"q_heads": 4, "max_rows": 0, "max_len": 0, "window": 0, "sinks": 0, "scale": 1.0}
+    a.update({k: v for k, v in change.items() if k in a})
+    return mx4._Attention(*a.values())
+
+
+@pytest.mark.parametrize("change,status", CACHES)
+def test_cache_shapes(L, change, status):
+    n = ctypes.c_size_t(0)
+    assert L.kv4_bytes(_cache(change), n) == status
+    assert L.kv4_bytes(_cache({}), None) == INVALID
+    assert L.kv4_bytes(None, n) == INVALID
+
+
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_cache_bytes_are_4_25_bits_per_element(L, head_dim):
+    n = ctypes.c_size_t(0)
+    assert L.kv4_bytes(_cache({"head_dim": head_dim}), n) == OK
+    assert n.value * 8 == 4 * 2 * 64 * 2 * head_dim * 4.25
+
+
+@pytest.mark.parametrize("change,status", CACHES + ROWS)
+def test_append_and_read(L, change, status):
+    strides = (ctypes.c_int64 * 4)(128, 64, 128, 64)
+    c, r = _cache(change), _rows(change)
+    assert L.kv4_append(None, c, r, P, P, ecw.DT_BF16, strides) == status
+    assert L.kv4_read(None, c, r, P, P, ecw.DT_BF16) == status
+
+
+def test_append_and_read_operands(L):
+    strides = (ctypes.c_int64 * 4)(128, 64, 128, 64)
+    c, r = _cache({}), _rows({})
+    for k, v, dt, st in ((0, P, ecw.DT_BF16, strides), (P, P + 1, ecw.DT_BF16, strides), (P, P, ecw.DT_I8, strides),
+                         (P, P, ecw.DT_BF16, None), (P, P + 2, ecw.DT_F32, strides),
+                         (P, P, ecw.DT_F16, (ctypes.c_int64 * 4)(128, 64, -128, 64))):
+        assert L.kv4_append(None, c, r, k, v, dt, st) == INVALID
+    for k, v, dt in ((0, P, ecw.DT_BF16), (P, P + 8, ecw.DT_BF16), (P, P, ecw.DT_I8)):
+        assert L.kv4_read(None, c, r, k, v, dt) == INVALID
+    assert L.kv4_append(None, c, None, P, P, ecw.DT_BF16, strides) == INVALID
+
+
+@pytest.mark.parametrize("change,status", CACHES + ROWS + TIMES)
+def test_attend(L, change, status):
+    n = ctypes.c_size_t(0)
+    c, r, a = _cache(change), _rows(change), _attention(change)
+    assert L.kv4_attend_workspace_size(c, r, a, n) == status
+    assert L.kv4_attend(None, c, r, a, P, ecw.DT_BF16, 256, 64, P, P, 1 << 30) == status
+
+
+def test_attend_operands_and_workspace(L):
+    n = ctypes.c_size_t(0)
+    c, r, a = _cache({}), _rows({"table_width": 4096}), _attention({})
+    assert L.kv4_attend_workspace_size(c, r, a, n) == OK and n.value > 0
+    for q, dt, row, head, o, ws, size in (
+            (0, ecw.DT_BF16, 256, 64, P, P, n.value), (P + 1, ecw.DT_BF16, 256, 64, P, P, n.value),
+            (P, ecw.DT_F32, 256, 64, P, P, n.value), (P, ecw.DT_BF16, -1, 64, P, P, n.value),
+            (P, ecw.DT_BF16, 256, 64, 0, P, n.value), (P, ecw.DT_BF16, 256, 64, P + 8, P, n.value),
+            (P, ecw.DT_BF16, 256, 64, P, 0, n.value), (P, ecw.DT_BF16, 256, 64, P, P + 4, n.value),
+            (P, ecw.DT_BF16, 256, 64, P, P, n.value - 1)):
+        assert L.kv4_attend(None, c, r, a, q, dt, row, head, o, ws, size) == INVALID
+    assert L.kv4_attend(None, c, r, None, P, ecw.DT_BF16, 256, 64, P, P, n.value) == INVALID
+
+
+def test_tensors_off_the_gpu_are_refused():
+    with pytest.raises(TypeError):
+        ecw.mx4_quantize(torch.zeros(2, 64))
+    with pytest.raises(TypeError):
+        ecw.MX4Tensor(torch.zeros(2, 64, dtype=torch.uint8), torch.zeros(2, 4, dtype=torch.uint8), 2, 128)
+    with pytest.raises(ValueError):
+        ecw.KV4Cache(0, 1, 64)
