@@ -217,10 +217,6 @@ __device__ __forceinline__ void load_tile(Tile<NB>& t, const uint8_t* region, ui
   }
 }
 
-__device__ __forceinline__ bool has_nan_scale(uint32_t w) {  // a byte of 255
-  return (((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u) != 0;
-}
-
 // the operand of V^T for dimensions 2 B and 2 B + 1 of the lane's group: byte B of each
 // of the eight tokens, turned from pairs of dimensions into pairs of tokens
 template <int NB, int B>

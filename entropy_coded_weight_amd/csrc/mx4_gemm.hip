@@ -11,8 +11,9 @@
 // Sums are held in fp32.  4-bit values times a power of two are exact in bf16, so bf16
 // x needs no rounding.  In fp16 they are exact relative to the span's largest scale
 // when its scales span at most 2^23 (0.5 * 2^-23 is fp16's smallest number); the
-// span's sum is multiplied by that scale in fp32.  A wider span, or a NaN block, takes
-// x as the sum of two bf16 numbers, which holds every fp16 number exactly.
+// span's sum is multiplied by that scale in fp32.  A wider span takes further passes.
+#include <type_traits>
+
 #include "mx4_common.h"
 
 namespace ecw {
@@ -26,17 +27,29 @@ struct GemmArgs {
   const uint8_t* xs;      // scale bytes of 4-bit x
   void* y;
   int64_t x_stride;       // elements (16-bit x)
-  uint32_t rows, cols, batch, blocks;  // of w; blocks of a padded row
+  uint32_t rows, cols, batch;
+  uint32_t blocks, scales;  // of a padded row: blocks of codes, bytes of scales
   bool vec;               // rows of x are 16-byte aligned
 };
 
-__device__ __forceinline__ void store_y(void* y, uint64_t at, float v, int dt) {
-  if (dt == ECW_DT_F32)
+template <int DT>
+__device__ __forceinline__ void store_y(void* y, uint64_t at, float v) {
+  if constexpr (DT == ECW_DT_F32)
     static_cast<float*>(y)[at] = v;
-  else if (dt == ECW_DT_F16)
+  else if constexpr (DT == ECW_DT_F16)
     static_cast<_Float16*>(y)[at] = (_Float16)v;
   else
     static_cast<__bf16*>(y)[at] = (__bf16)v;
+}
+// f<DT>() for the output's type
+template <class F>
+__device__ __forceinline__ void with_type(int dt, F&& f) {
+  if (dt == ECW_DT_F32)
+    f(std::integral_constant<int, ECW_DT_F32>{});
+  else if (dt == ECW_DT_F16)
+    f(std::integral_constant<int, ECW_DT_F16>{});
+  else
+    f(std::integral_constant<int, ECW_DT_BF16>{});
 }
 
 // the largest and smallest byte of a word
@@ -44,6 +57,14 @@ __device__ __forceinline__ void byte_range(uint32_t w, uint32_t* lo, uint32_t* h
   const uint32_t a = w & 255, b = w >> 8 & 255, c = w >> 16 & 255, d = w >> 24;
   *hi = max(max(a, b), max(c, d));
   *lo = min(min(a, b), min(c, d));
+}
+// a word without its bytes of `from` or more
+__device__ __forceinline__ uint32_t bytes_below(uint32_t w, uint32_t from) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    if ((w >> i & 255) < from) r |= w & 255u << i;
+  return r;
 }
 
 // acc[t] += x tile t (rows: 16 of x) times a wave's 16 rows of w over one span.
@@ -61,17 +82,27 @@ __device__ __forceinline__ void span_product(f32x4 (&acc)[NT], u32x4 w, uint32_t
         acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[t][j]), b, acc[t], 0, 0, 0);
     }
   } else {
-    uint32_t lo, hi;
-    byte_range(sw, &lo, &hi);
+    // one pass, or with scales further apart one for each group of blocks within 2^23 of
+    // the largest left; NaN blocks go with the first
     const uint32_t mine = sw >> 8 * g & 255;
-    if (!__any(hi - lo > 23 || hi == kScaleNaN)) {
+    bool nan = mine == kScaleNaN;
+    uint32_t left = __any(has_nan_scale(sw)) ? bytes_below(sw, kScaleNaN) : sw, lo, hi;
+    bool several = false;
+    while (true) {
+      byte_range(left, &lo, &hi);
+      several = several || __any(hi - lo > 23);
+      u32x4 c = w;
+      if (several) {
+        const uint32_t my = left >> 8 * g & 255;
+        if (!nan && (my == 0 || my + 23 < hi)) c = u32x4{0, 0, 0, 0};
+      }
+      const float s = nan ? scale_of(kScaleNaN) : scale_of(min(max(mine + 126, hi) + 1 - hi, kScaleOne));
       f32x4 sum[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const float s = scale_of(kScaleOne + mine - hi);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f16x8 b = oct_f16(w[j], s);
+        const f16x8 b = oct_f16(c[j], s);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x[t][j]), b, sum[t], 0, 0, 0);
@@ -81,19 +112,10 @@ __device__ __forceinline__ void span_product(f32x4 (&acc)[NT], u32x4 w, uint32_t
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(sum[t][r], top, acc[t][r]);
-    } else {
-      const float s = scale_of(mine);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8 b = oct_bf16(w[j], s);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          bf16x8 h, l;
-          split_f16(x[t][j], &h, &l);
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, b, acc[t], 0, 0, 0);
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(l, b, acc[t], 0, 0, 0);
-        }
-      }
+      if (!several) break;
+      nan = false;
+      left = bytes_below(left, hi > 23 ? hi - 23 : 0);
+      if (!__any(left != 0)) break;
     }
   }
 }
@@ -117,7 +139,7 @@ __global__ void __launch_bounds__(1024) k_mx4_gemm_few(GemmArgs a, int y_dtype) 
   const uint32_t n = min(n0 + r16, a.rows - 1);
   const uint32_t spans = a.blocks / 4;
   const uint8_t* w = a.w + (uint64_t)n * a.blocks * 16 + g * 16;
-  const uint8_t* ws = a.ws + (uint64_t)n * a.blocks;
+  const uint8_t* ws = a.ws + (uint64_t)n * a.scales;
   f32x4 acc[NT];
   uint64_t m[NT];
 #pragma unroll
@@ -132,7 +154,7 @@ __global__ void __launch_bounds__(1024) k_mx4_gemm_few(GemmArgs a, int y_dtype) 
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint8_t* x = static_cast<const uint8_t*>(a.x) + m[t] * a.blocks * 16 + (uint64_t)s * 64 + g * 16;
-        const uint32_t sx = *reinterpret_cast<const uint32_t*>(a.xs + m[t] * a.blocks + s * 4);
+        const uint32_t sx = *reinterpret_cast<const uint32_t*>(a.xs + m[t] * a.scales + s * 4);
         acc[t] = span_product_mx4(acc[t], wv, sw, g, *reinterpret_cast<const u32x4*>(x), sx);
       }
     } else {
@@ -156,8 +178,277 @@ __global__ void __launch_bounds__(1024) k_mx4_gemm_few(GemmArgs a, int y_dtype) 
     const uint32_t row = n0 + (i & 15), b = m0 + i / 64 * 16 + (i >> 4 & 3) * 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (row < a.rows && b + r < a.batch) store_y(a.y, (uint64_t)(b + r) * a.rows + row, sum[r], y_dtype);
+      if (row < a.rows && b + r < a.batch) with_type(y_dtype, [&](auto dt) { store_y<dt.value>(a.y, (uint64_t)(b + r) * a.rows + row, sum[r]); });
   }
+}
+
+// A block's place among the tiles: blocks go to the 8 dies in turn, so each die takes a
+// contiguous run of tiles, and within it 8 tiles of x rows stand next to each other, for
+// the die's L2 to hold what its blocks share.
+__device__ __forceinline__ void tile_of(uint32_t m_tiles, uint32_t n_tiles, uint32_t* m, uint32_t* n) {
+  const uint32_t all = m_tiles * n_tiles, per = all / 8, more = all % 8;
+  const uint32_t die = blockIdx.x % 8, i = blockIdx.x / 8;
+  const uint32_t id = die * per + min(die, more) + i;
+  const uint32_t band = id / (8 * n_tiles), first = band * 8, high = min(8u, m_tiles - first);
+  const uint32_t in = id - band * 8 * n_tiles;
+  *m = first + in % high;
+  *n = in / high;
+}
+
+// Where a row's 16 column octets of a span lie in LDS: octet o of row r at place
+// turned(o) ^ (r % 16), so that neither a row written nor a column read by 16 lanes meets
+// a bank twice (LDS serves lanes 0-3, 12-15 and 20-27 of a wave together).
+__device__ __forceinline__ uint32_t turned(uint32_t o) { return (o & 3) * 4 + (o >> 2); }
+
+// For x whose rows are not 16-byte aligned: 128 rows of x by 128 rows of w per block, 64
+// by 64 per wave, x through registers into LDS, w straight into registers.  The next
+// span's loads are in flight while a span is multiplied.
+template <int ACT>
+__global__ void __launch_bounds__(256, 2) k_mx4_gemm_loose(GemmArgs a, uint32_t m_tiles, uint32_t n_tiles, int y_dtype) {
+  __shared__ u32x4 lds[2][128 * 16];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t r16 = lane & 15, g = lane >> 4;
+  uint32_t mt, nt;
+  tile_of(m_tiles, n_tiles, &mt, &nt);
+  const uint32_t m0 = mt * 128, n0 = nt * 128 + (wave & 1) * 64, mw = (wave >> 1) * 64;
+  const uint32_t spans = a.blocks / 4;
+
+  // this thread's part of an x span: one octet of rows threadIdx / 16 + 16 i
+  const uint32_t oct = turned(threadIdx.x & 15), row = threadIdx.x >> 4;
+  const uint16_t* x[8];
+  u32x4 xs[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = static_cast<const uint16_t*>(a.x) + (int64_t)min(m0 + row + 16 * i, a.batch - 1) * a.x_stride;
+  const uint8_t* w[4];
+  const uint8_t* ws[4];
+  u32x4 wv[4];
+  uint32_t sw[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const uint32_t at = min(n0 + n * 16 + r16, a.rows - 1);
+    w[n] = a.w + (uint64_t)at * a.blocks * 16 + g * 16;
+    ws[n] = a.ws + (uint64_t)at * a.scales;
+  }
+  auto load_x = [&](uint32_t s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) xs[i] = load_oct16(x[i], s * 128 + oct * 8, a.cols, a.vec).v;
+  };
+  auto load_w = [&](uint32_t s) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      wv[n] = *reinterpret_cast<const u32x4*>(w[n] + (uint64_t)s * 64);
+      sw[n] = *reinterpret_cast<const uint32_t*>(ws[n] + s * 4);
+    }
+  };
+  auto store_x = [&](uint32_t buf) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lds[buf][(row + 16 * i) * 16 + ((threadIdx.x & 15) ^ row)] = xs[i];
+  };
+
+  f32x4 acc[4][4];  // [n][m]
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  load_x(0);
+  load_w(0);
+  store_x(0);
+  __syncthreads();
+  for (uint32_t s = 0; s < spans; ++s) {
+    u32x4 wn[4];
+    uint32_t sn[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) wn[n] = wv[n], sn[n] = sw[n];
+    if (s + 1 < spans) {
+      load_x(s + 1);
+      load_w(s + 1);
+    }
+    u32x4 xf[4][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xf[m][j] = lds[s & 1][(mw + m * 16 + r16) * 16 + ((4 * j + g) ^ r16)];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) span_product<ACT, 4>(acc[n], wn[n], sn[n], g, xf);
+    if (s + 1 < spans) store_x((s + 1) & 1);
+    __syncthreads();
+  }
+  with_type(y_dtype, [&](auto dt) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t b = m0 + mw + m * 16 + g * 4 + r, at = n0 + n * 16 + r16;
+          if (b < a.batch && at < a.rows) store_y<dt.value>(a.y, (uint64_t)b * a.rows + at, acc[n][m][r]);
+        }
+  });
+}
+
+// ------------------------------------------------------------------ many rows
+// Copies 16 (or 4) bytes per lane from global memory to LDS, lane after lane from `to`
+// on, without registers between.  The caller counts them: they are done when
+// `s_waitcnt vmcnt` says so.
+template <int BYTES>
+__device__ __forceinline__ void to_lds(const void* from, uint32_t to) {
+  static_assert(BYTES == 16 || BYTES == 4, "");
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+__device__ const u32x4 zeros16 = {0, 0, 0, 0};
+
+// 16 rows of 4 bits of a span are 1 KiB in LDS: row r's block b at place 4 r + (b ^
+// shifted(r)), so that four neighbouring lanes copy 64 neighbouring bytes and the 16
+// lanes that LDS serves together meet no bank twice.
+__device__ __forceinline__ uint32_t shifted(uint32_t r) { return (0u - (r >> 2)) & 3; }
+
+// A block of WM x WN waves multiplies 16 TM WM rows of x and 16 TN WN rows of w, a span
+// at a time, from NS stages in LDS that copies fill NS - 1 spans ahead.  Scales come for
+// four spans at once, into two places of their own.
+template <int ACT, int WM, int WN, int TM, int TN, int NS>
+struct Tiles {
+  static constexpr bool kX4 = ACT == kActMX4;
+  static constexpr int kWaves = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
+  static constexpr uint32_t kX = kX4 ? BM * 64 : BM * 256, kW = BN * 64, kStage = kX + kW;
+  static constexpr uint32_t kScaleRows = (kX4 ? BM : 0) + BN;  // those of x first
+  static constexpr uint32_t kBytes = kStage * NS + 2 * kScaleRows * 16;
+  static constexpr int kXLoads = kX / 1024 / kWaves, kWLoads = kW / 1024 / kWaves;  // copies per wave and span
+  static constexpr int kSLoads = (kScaleRows / 64 + kWaves - 1) / kWaves;           // per four spans
+  static_assert(kX % (1024 * kWaves) == 0 && kW % (1024 * kWaves) == 0 && NS <= 5, "");
+  static_assert(kBytes <= 160 * 1024, "");
+};
+
+template <int ACT, int WM, int WN, int TM, int TN, int NS>
+__global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint32_t m_tiles, uint32_t n_tiles,
+                                                                int y_dtype) {
+  using T = Tiles<ACT, WM, WN, TM, TN, NS>;
+  __shared__ __align__(16) uint8_t lds[T::kBytes];
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r16 = lane & 15, g = lane >> 4;
+  uint32_t mt, nt;
+  tile_of(m_tiles, n_tiles, &mt, &nt);
+  const uint32_t m0 = mt * T::BM, n0 = nt * T::BN, spans = a.blocks / 4;
+
+  const uint8_t *xp[T::kXLoads], *wp[T::kWLoads], *sp[T::kSLoads];
+  const uint32_t r4 = lane >> 2, b4 = (lane & 3) ^ shifted(r4);  // row and block that the lane copies of 16 rows
+#pragma unroll
+  for (int i = 0; i < T::kXLoads; ++i) {
+    const uint32_t part = wave * T::kXLoads + i;  // 1 KiB: 16 rows of 4 bits, or 4 rows of 16 bits
+    if constexpr (T::kX4) {
+      xp[i] = static_cast<const uint8_t*>(a.x) + (uint64_t)min(m0 + part * 16 + r4, a.batch - 1) * a.blocks * 16 + b4 * 16;
+    } else {
+      const uint32_t row = part * 4 + g;
+      const uint32_t oct = turned(r16 ^ (row & 15));
+      xp[i] = static_cast<const uint8_t*>(a.x) + (int64_t)min(m0 + row, a.batch - 1) * a.x_stride * 2 + oct * 16;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < T::kWLoads; ++i)
+    wp[i] = a.w + (uint64_t)min(n0 + (wave * T::kWLoads + i) * 16 + r4, a.rows - 1) * a.blocks * 16 + b4 * 16;
+#pragma unroll
+  for (int i = 0; i < T::kSLoads; ++i) {
+    const uint32_t row = (wave + i * T::kWaves) * 64 + lane;
+    if (T::kX4 && row < T::BM)
+      sp[i] = a.xs + (uint64_t)min(m0 + row, a.batch - 1) * a.scales;
+    else
+      sp[i] = a.ws + (uint64_t)min(n0 + row - (T::kX4 ? T::BM : 0), a.rows - 1) * a.scales;
+  }
+
+  // copies of one span into a stage; past the last span the last one again, into a stage
+  // that nothing reads, so that every turn waits for the same number
+  auto fill = [&](uint32_t span, uint32_t stage) {
+    const uint64_t s = min(span, spans - 1);
+    if (span % 4 == 0 && span < spans) {
+#pragma unroll
+      for (int i = 0; i < T::kSLoads; ++i) {
+        const uint32_t part = wave + i * T::kWaves;
+        if (part < T::kScaleRows / 64)
+          to_lds<16>(sp[i] + s * 4, base + T::kStage * NS + (span / 4 % 2) * T::kScaleRows * 16 + part * 1024);
+      }
+    }
+    const uint32_t to = base + stage * T::kStage;
+#pragma unroll
+    for (int i = 0; i < T::kXLoads; ++i) {
+      const uint32_t part = wave * T::kXLoads + i;
+      const uint8_t* from = xp[i] + s * (T::kX4 ? 64 : 256);
+      if constexpr (!T::kX4) {
+        const uint32_t oct = turned(r16 ^ ((part * 4 + g) & 15));
+        if ((uint32_t)s * 128 + oct * 8 >= a.cols) from = reinterpret_cast<const uint8_t*>(&zeros16);
+      }
+      to_lds<16>(from, to + part * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < T::kWLoads; ++i) to_lds<16>(wp[i] + s * 64, to + T::kX + (wave * T::kWLoads + i) * 1024);
+  };
+
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int n = 0; n < TN; ++n)
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint32_t wm = wave / WN * TM, wn = wave % WN * TN;  // first 16-row tiles of the wave
+
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) fill(i, i);
+  uint32_t stage = 0, next = NS - 1;
+  for (uint32_t s = 0; s < spans; ++s) {
+    wait_copies<(NS - 2) * (T::kXLoads + T::kWLoads)>();  // or fewer left, if scales are among them
+    __builtin_amdgcn_s_barrier();  // this span is there, and the one before it is done with
+    fill(s + NS - 1, next);
+    const uint8_t* at = lds + stage * T::kStage;
+    const u32x4* x = reinterpret_cast<const u32x4*>(at);
+    const u32x4* w = reinterpret_cast<const u32x4*>(at + T::kX);
+    const uint32_t* xs = reinterpret_cast<const uint32_t*>(lds + T::kStage * NS + (s / 4 % 2) * T::kScaleRows * 16) + s % 4;
+    const uint32_t* ws = xs + (T::kX4 ? T::BM * 4 : 0);
+    const uint32_t in = r16 * 4 + (g ^ shifted(r16));  // the lane's place in 16 rows of 4 bits
+    if constexpr (T::kX4) {
+      u32x4 xf[TM];
+      uint32_t xb[TM];
+#pragma unroll
+      for (int m = 0; m < TM; ++m) xf[m] = x[(wm + m) * 64 + in], xb[m] = xs[((wm + m) * 16 + r16) * 4];
+#pragma unroll
+      for (int n = 0; n < TN; ++n) {
+        const u32x4 wf = w[(wn + n) * 64 + in];
+        const uint32_t wb = ws[((wn + n) * 16 + r16) * 4];
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[n][m] = span_product_mx4(acc[n][m], wf, wb, g, xf[m], xb[m]);
+      }
+    } else {
+      u32x4 xf[TM][4];
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xf[m][j] = x[((wm + m) * 16 + r16) * 16 + ((4 * j + g) ^ r16)];
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+        span_product<ACT, TM>(acc[n], w[(wn + n) * 64 + in], ws[((wn + n) * 16 + r16) * 4], g, xf);
+    }
+    stage = stage + 1 == NS ? 0 : stage + 1;
+    next = next + 1 == NS ? 0 : next + 1;
+  }
+  wait_copies<0>();
+  with_type(y_dtype, [&](auto dt) {
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t b = m0 + (wm + m) * 16 + g * 4 + r, at = n0 + (wn + n) * 16 + r16;
+          if (b < a.batch && at < a.rows) store_y<dt.value>(a.y, (uint64_t)b * a.rows + at, acc[n][m][r]);
+        }
+  });
 }
 
 }  // namespace ecw
@@ -185,10 +476,32 @@ ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   return launched("mx4_gemm");
 }
 
+template <int ACT, int WM, int WN, int TM, int TN, int NS>
+ecw_status launch_tile(hipStream_t stream, const GemmArgs& a, int y_dtype) {
+  using T = Tiles<ACT, WM, WN, TM, TN, NS>;
+  const uint32_t m_tiles = (a.batch + T::BM - 1) / T::BM, n_tiles = (a.rows + T::BN - 1) / T::BN;
+  if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
+  hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves), 0,
+                     stream, a, m_tiles, n_tiles, y_dtype);
+  return launched("mx4_gemm");
+}
+
 template <int ACT>
 ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   if (a.batch <= 16) return launch_few<ACT, 1>(stream, a, y_dtype);
   if (a.batch <= 32) return launch_few<ACT, 2>(stream, a, y_dtype);
+  if (a.batch > 64) {
+    if constexpr (ACT == kActMX4) {
+      return launch_tile<ACT, 2, 4, 8, 4, 4>(stream, a, y_dtype);
+    } else {
+      if (a.vec && a.cols % 8 == 0) return launch_tile<ACT, 2, 4, 4, 2, 3>(stream, a, y_dtype);
+      const uint32_t m_tiles = (a.batch + 127) / 128, n_tiles = (a.rows + 127) / 128;
+      if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
+      hipLaunchKernelGGL(k_mx4_gemm_loose<ACT>, dim3(m_tiles * n_tiles), dim3(256), 0, stream, a, m_tiles, n_tiles,
+                         y_dtype);
+      return launched("mx4_gemm");
+    }
+  }
   return launch_few<ACT, 4>(stream, a, y_dtype);
 }
 
@@ -215,7 +528,7 @@ ecw_status mx4_gemm(ecw_stream stream, const void* w_codes, const void* w_scales
   if (!x || !aligned(x, 2) || x_stride < 0)
     return refuse(ECW_E_INVALID_ARG, "x must be an aligned device pointer with a row stride of 0 or more");
   const GemmArgs a{static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales), x, nullptr, y,
-                   x_stride, rows, cols, batch, row_blocks(cols), aligned(x, 16) && x_stride % 8 == 0};
+                   x_stride, rows, cols, batch, row_blocks(cols), scale_stride(cols), aligned(x, 16) && x_stride % 8 == 0};
   return x_dtype == ECW_DT_F16 ? launch<ECW_DT_F16>((hipStream_t)stream, a, y_dtype)
                                : launch<ECW_DT_BF16>((hipStream_t)stream, a, y_dtype);
 }
@@ -228,7 +541,7 @@ ecw_status mx4_gemm_mx4(ecw_stream stream, const void* w_codes, const void* w_sc
   if (rows == 0 || batch == 0) return ECW_OK;
   if (ecw_status s = check_output(y, y_dtype, batch)) return s;
   const GemmArgs a{static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales), x_codes,
-                   static_cast<const uint8_t*>(x_scales), y, 0, rows, cols, batch, row_blocks(cols), true};
+                   static_cast<const uint8_t*>(x_scales), y, 0, rows, cols, batch, row_blocks(cols), scale_stride(cols), true};
   return launch<kActMX4>((hipStream_t)stream, a, y_dtype);
 }
 

@@ -37,7 +37,13 @@ __global__ void __launch_bounds__(256) k_mx4_quantise(const void* __restrict__ x
     c = quantise_oct<DT == ECW_DT_F16>(
         load_oct16(static_cast<const uint16_t*>(x) + row * stride, oct * 8, cols, vec), &b);
   codes[at] = c;
-  if ((oct & 3) == 0) scales[at >> 2] = (uint8_t)b;
+  if ((oct & 3) == 0) {
+    const uint32_t stride = scale_stride(cols), block = oct >> 2, blocks = octs >> 2;
+    uint8_t* to = scales + (uint64_t)row * stride + block;
+    *to = (uint8_t)b;
+    if (block == blocks - 1)  // the rest of the last 16 bytes
+      for (uint32_t i = blocks; i < stride; ++i) *++to = kScaleOne;
+  }
 }
 
 template <int DT>
@@ -48,7 +54,8 @@ __global__ void __launch_bounds__(256) k_mx4_dequantise(const uint32_t* __restri
   const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
   const uint32_t row = (uint32_t)(at / octs), oct = (uint32_t)(at - (uint64_t)row * octs);
   if (row >= rows || oct * 8 >= cols) return;
-  store_oct<DT>(out, (uint64_t)row * cols + oct * 8, codes[at], scale_of(scales[at >> 2]), cols - oct * 8, vec);
+  store_oct<DT>(out, (uint64_t)row * cols + oct * 8, codes[at],
+                scale_of(scales[(uint64_t)row * scale_stride(cols) + (oct >> 2)]), cols - oct * 8, vec);
 }
 
 }  // namespace ecw

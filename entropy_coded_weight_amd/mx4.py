@@ -107,19 +107,18 @@ def _ints(t, name, device, shape):
 class MX4Tensor:
     """A matrix [rows, cols] of 4-bit floats with a power-of-two scale per 32 columns.
 
-    codes: uint8 [rows, 64 * ceil(cols / 128)], scales: uint8 [rows, 4 * ceil(cols / 128)]
+    codes: uint8 [rows, 64 * ceil(cols / 128)], scales: uint8 [rows, 16 * ceil(cols / 512)]
     (the byte of each block's scale; 255: the block is NaN)."""
 
     __slots__ = ("codes", "scales", "rows", "cols")
 
     def __init__(self, codes, scales, rows, cols):
-        spans = (cols + 127) // 128
-        for name, t, per in (("codes", codes, 64), ("scales", scales, 4)):
+        for name, t, width in (("codes", codes, (cols + 127) // 128 * 64), ("scales", scales, (cols + 511) // 512 * 16)):
             _on_gpu(t, name)
             if t.dtype != torch.uint8 or not t.is_contiguous():
                 raise TypeError(f"{name} must be contiguous uint8")
-            if tuple(t.shape) != (rows, per * spans):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, per * spans)}")
+            if tuple(t.shape) != (rows, width):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
         if scales.device != codes.device:
             raise ValueError("codes and scales are on different devices")
         self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
@@ -201,10 +200,9 @@ def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None, stream=None) -> 
         used = (x,) if out is None else (x, out.codes, out.scales)
         return _elsewhere(dev, stream, used, lambda: mx4_quantize(x, out))
     if out is None:
-        spans = (cols + 127) // 128
         out = MX4Tensor.__new__(MX4Tensor)
-        out.codes = torch.empty((rows, 64 * spans), dtype=torch.uint8, device=dev)
-        out.scales = torch.empty((rows, 4 * spans), dtype=torch.uint8, device=dev)
+        out.codes = torch.empty((rows, (cols + 127) // 128 * 64), dtype=torch.uint8, device=dev)
+        out.scales = torch.empty((rows, (cols + 511) // 512 * 16), dtype=torch.uint8, device=dev)
         out.rows, out.cols = rows, cols
     elif out.shape != (rows, cols) or out.device != dev:
         raise ValueError(f"out must be a {(rows, cols)} MX4Tensor on {dev}")

@@ -372,7 +372,7 @@ uint32_t ecw_abi_version(void);
  *   elements round to nearest, ties to the even code; magnitudes over 6 become 6
  * A block with an infinity or a NaN has the byte 255 and stands for NaN.  Zeros past
  * the last column fill a row up to a multiple of 128 columns.
- *   codes  [rows][ceil(cols / 128) * 64] bytes     scales [rows][ceil(cols / 128) * 4] bytes
+ *   codes  [rows][ceil(cols / 128) * 64] bytes     scales [rows][ceil(cols / 512) * 16] bytes
  * both 16-byte aligned device memory.  No call needs zero-filled or persistent
  * workspace; calls with rows or batch of zero launch nothing.
  */
