@@ -154,30 +154,38 @@ __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __rest
 // transposed, so that no value crosses lanes between the two products: of
 // S^T = K q^T (16x16x32 instructions) lane l gets query l % 16 and tokens
 // 4 (l / 16) .. + 3 of each half tile, which is the operand of O^T += V^T P^T if that
-// instruction's order of tokens is taken the same way; the running maximum, sum and
-// rescaling then belong to the lane's own query column.
+// instruction's order of tokens is taken the same way.  A third product, of ones, sums
+// the weights as they were rounded.  Weights are 2^(scale s - c) with an offset c of the
+// lane's own query column that only moves when a weight would pass 2^8, so that most
+// tiles need neither a maximum across lanes nor a rescaling.
+//
+// With a bf16 query keys, values and weights are bf16; with an fp16 query fp16, which
+// holds keys and values exactly between scales of 2^-23 and 2^13, all that fp16 keys and
+// values can have.  Smaller ones round to multiples of 2^-24, larger ones count as NaN.
 struct AttendArgs {
   Cache c;
   Batch t;
   const uint16_t* q;
   void* o;
-  float* part;            // per split and row: dim fp32 of O; then per split and row: maximum and sum
+  float* part;            // per split and row: dim fp32 of O; then per split and row: offset and sum
   int64_t q_row, q_head;  // strides
   uint32_t group, q_heads, q_tiles, splits;
+  uint32_t chunk;         // tiles of one split
+  uint32_t per_page;      // 2^32 / tiles of a page, rounded up
   int32_t window, sinks;  // window 0: none
   float scale;            // times log2 e
   bool vec;
 };
 
-// A row's softmax state: its maximum (in powers of two) and sum.  kNothing as the sum:
-// no token was visible, so the output is zero; a sum of zero from tokens that were
-// visible (all scores -inf) gives NaN, as the definition does.
+// A row's softmax state: its offset and sum.  kNothing as the sum: no token was visible,
+// so the output is zero; a sum of zero from tokens that were visible (all scores -inf)
+// gives NaN, as the definition does.
 constexpr float kNothing = -1.f;
 
 template <int NB>
 struct Tile {  // what a lane holds of 32 tokens
   uint32_t k[2][NB], v[2][NB];
-  uint32_t ks[2][NB / 4 + 1], vs[2];
+  uint32_t ks[2], vs[2];  // scale bytes: of the lane's token and its NB octets; of its four tokens
 };
 
 template <int N>
@@ -194,7 +202,6 @@ __device__ __forceinline__ void load_words(uint32_t (&to)[N], const uint8_t* p) 
   }
 }
 
-// value scales of a lane's dimension group: block group * 2 NB / 32
 template <int NB>
 __device__ __forceinline__ void load_tile(Tile<NB>& t, const uint8_t* region, uint32_t page_tokens, uint32_t at,
                                           uint32_t r16, uint32_t g) {
@@ -206,42 +213,77 @@ __device__ __forceinline__ void load_tile(Tile<NB>& t, const uint8_t* region, ui
     const uint32_t token = at + 16 * h;
     load_words<NB>(t.k[h], region + (token + r16) * (NB * 16) + g * (NB * 4));
     load_words<NB>(t.v[h], v + ((token / 4 + g) * 16 + r16) * (NB * 4));
-    // the lane's NB octets of dimensions g NB .. lie in blocks g NB / 4 ..
-    if constexpr (NB == 8) {
-      const uint32_t two = *reinterpret_cast<const uint16_t*>(ks + (token + r16) * NB + g * 2);
-      t.ks[h][0] = two & 255, t.ks[h][1] = two >> 8;
-    } else {
-      t.ks[h][0] = ks[(token + r16) * NB + g * NB / 4];
-    }
+    // the lane's NB octets of dimensions, from g NB on, lie in the blocks from g NB / 4 on
+    if constexpr (NB == 8)
+      t.ks[h] = *reinterpret_cast<const uint16_t*>(ks + (token + r16) * NB + g * 2);
+    else
+      t.ks[h] = ks[(token + r16) * NB + g * NB / 4];
     t.vs[h] = *reinterpret_cast<const uint32_t*>(vs + ((token / 4 + g) * NB + r16 * NB / 16) * 4);
   }
 }
 
-// the operand of V^T for dimensions 2 B and 2 B + 1 of the lane's group: byte B of each
+// eight elements of 16-bit type, as the matrix instructions take them
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <bool F16>
+__device__ __forceinline__ u32x4 oct(uint32_t codes, float scale) {
+  if constexpr (F16)
+    return __builtin_bit_cast(u32x4, oct_f16(codes, scale));
+  else
+    return __builtin_bit_cast(u32x4, oct_bf16(codes, scale));
+}
+template <bool F16, int SEL>
+__device__ __forceinline__ uint32_t pair(uint32_t codes, float scale) {
+  if constexpr (F16)
+    return pair_f16<SEL>(codes, scale);
+  else
+    return pair_bf16<SEL>(codes, scale);
+}
+template <bool F16>
+__device__ __forceinline__ u32x4 round8(const float (&x)[8]) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F16)
+      r[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)x[2 * i], (_Float16)x[2 * i + 1]});
+    else
+      r[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[2 * i], (__bf16)x[2 * i + 1]});
+  }
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ u32x4 ones() {
+  const uint32_t w = F16 ? 0x3c003c00u : 0x3f803f80u;
+  return u32x4{w, w, w, w};
+}
+
+// the operands of V^T for dimensions 2 B and 2 B + 1 of the lane's group: byte B of each
 // of the eight tokens, turned from pairs of dimensions into pairs of tokens
-template <int NB, int B>
-__device__ __forceinline__ void value_operands(const Tile<NB>& t, const float (&s)[8], bf16x8* even, bf16x8* odd) {
+template <bool F16, int NB, int B>
+__device__ __forceinline__ void value_operands(const Tile<NB>& t, const float (&s)[8], u32x4* even, u32x4* odd) {
   uint32_t p[8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if constexpr (NB == 2) {  // two tokens a word
-      p[4 * h] = pair_bf16<B>(t.v[h][0], s[4 * h]);
-      p[4 * h + 1] = pair_bf16<2 + B>(t.v[h][0], s[4 * h + 1]);
-      p[4 * h + 2] = pair_bf16<B>(t.v[h][1], s[4 * h + 2]);
-      p[4 * h + 3] = pair_bf16<2 + B>(t.v[h][1], s[4 * h + 3]);
+      p[4 * h] = pair<F16, B>(t.v[h][0], s[4 * h]);
+      p[4 * h + 1] = pair<F16, 2 + B>(t.v[h][0], s[4 * h + 1]);
+      p[4 * h + 2] = pair<F16, B>(t.v[h][1], s[4 * h + 2]);
+      p[4 * h + 3] = pair<F16, 2 + B>(t.v[h][1], s[4 * h + 3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[4 * h + i] = pair_bf16<B % 4>(t.v[h][i * (NB / 4) + B / 4], s[4 * h + i]);
+      for (int i = 0; i < 4; ++i) p[4 * h + i] = pair<F16, B % 4>(t.v[h][i * (NB / 4) + B / 4], s[4 * h + i]);
     }
   }
-  u32x4 e, o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    e[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x05040100u);
-    o[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x07060302u);
+    (*even)[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x05040100u);
+    (*odd)[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x07060302u);
   }
-  *even = __builtin_bit_cast(bf16x8, e);
-  *odd = __builtin_bit_cast(bf16x8, o);
 }
 
 template <int I, int N, class F>
@@ -254,95 +296,18 @@ __device__ __forceinline__ void each(F&& f) {
 
 template <int NB, int NQ, bool F16>
 struct Wave {
-  bf16x8 q[NQ][NB], ql[F16 ? NQ : 1][F16 ? NB : 1];
+  // fp16 weights stand 2^7 higher than bf16's: fp16 ends at 2^15, and what is lost at its
+  // other end is then under 2^-31 of the largest weight
+  static constexpr float kTop = F16 ? 7.f : 0.f, kSlack = 8.f;
+
+  u32x4 q[NQ][NB];
   int32_t pos[NQ];  // of the lane's query row in each tile, -1: no row
-  f32x4 o[NQ][2 * NB];
-  float m[NQ], l[NQ];
+  f32x4 o[NQ][2 * NB], l[NQ];
+  float c[NQ], most[NQ];  // offset; largest exponent that it allows, -inf: none yet
   bool seen[NQ];
 
   __device__ __forceinline__ bool visible(const AttendArgs& a, int32_t t, int32_t p) const {
     return t <= p && (a.window == 0 || t > p - a.window || t < a.sinks);
-  }
-
-  // One tile of tokens from t0 on; whole: every row sees every token.
-  __device__ __forceinline__ void tile(const AttendArgs& a, Tile<NB>& t, int32_t t0, bool whole, int32_t stored,
-                                       uint32_t g) {
-    f32x4 s[2][NQ];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const bf16x8 k = oct_bf16(t.k[h][j], scale_of(t.ks[h][j / 4]));
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          s[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[n][j], s[h][n], 0, 0, 0);
-          if constexpr (F16) s[h][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, ql[n][j], s[h][n], 0, 0, 0);
-        }
-      }
-    }
-    // tokens past the last one stored hold anything: as zeros they add nothing
-    if (t0 + 32 > stored) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t0 + 16 * h + 4 * (int32_t)g + i >= stored) clear_value(t, h, i);
-    }
-    bf16x8 p[NQ];
-    uint32_t vis[NQ];  // bits: the lane's eight tokens
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      float x[8], top = -INFINITY;
-      vis[n] = 0xff;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = s[i / 4][n][i % 4] * a.scale;
-      if (!whole) {
-        vis[n] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (visible(a, t0 + 16 * (i / 4) + 4 * (int32_t)g + i % 4, pos[n])) vis[n] |= 1u << i;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (!(vis[n] >> i & 1)) x[i] = -INFINITY;
-      }
-      seen[n] |= vis[n] != 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float now = fmaxf(m[n], top), base = now == -INFINITY ? 0.f : now;
-      const float fade = __builtin_amdgcn_exp2f(m[n] - base);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = __builtin_amdgcn_exp2f(x[i] - base);
-        sum += x[i];
-      }
-      // the weights are rounded to bf16, 2^-9 of each, for the second product; their sum is not
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[n][i] = (__bf16)x[i];
-      l[n] = l[n] * fade + sum;
-      if (__any(now != m[n])) {
-#pragma unroll
-        for (int d = 0; d < 2 * NB; ++d) o[n][d] *= fade;
-      }
-      m[n] = now;
-    }
-    if (__any(has_nan_scale(t.vs[0]) || has_nan_scale(t.vs[1]))) mark_nan(t, vis);
-    float vs[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) vs[i] = scale_of(t.vs[i / 4] >> 8 * (i % 4) & 255);
-    each<0, NB>([&](auto b) {
-      bf16x8 even, odd;
-      value_operands<NB, b.value>(t, vs, &even, &odd);
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        o[n][2 * b.value] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, p[n], o[n][2 * b.value], 0, 0, 0);
-        o[n][2 * b.value + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, p[n], o[n][2 * b.value + 1], 0, 0, 0);
-      }
-    });
   }
 
   // A token's value as zeros of scale 1; i: the token among the lane's four of half h.
@@ -356,16 +321,73 @@ struct Wave {
     t.vs[h] = (t.vs[h] & ~(255u << 8 * i)) | kScaleOne << 8 * i;
   }
 
-  // Value blocks that are NaN: a weight of zero times NaN must not reach rows that do not
-  // see the token, so these blocks count as zeros, and the rows that see one become NaN
-  // in its dimensions.  A product of ones marks them.
-  __device__ __forceinline__ void mark_nan(Tile<NB>& t, const uint32_t (&vis)[NQ]) {
+  __device__ __forceinline__ void scores(const Tile<NB>& t, f32x4 (&s)[2][NQ]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const u32x4 k = oct<F16>(t.k[h][j], scale_of(t.ks[h] >> 8 * (j / 4) & 255));
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) s[h][n] = mfma16<F16>(k, q[n][j], s[h][n]);
+      }
+    }
+  }
+
+  // The weights of a tile's scores for query tile n, rounded to the product's type (half a
+  // step of each), and which of the lane's eight tokens count.
+  __device__ __forceinline__ u32x4 weights(const AttendArgs& a, const f32x4 (&s)[2][NQ], int n, int32_t t0, bool whole,
+                                           uint32_t g, uint32_t& vis) {
+    float p[8];
+    vis = 0xff;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = fmaf(s[i / 4][n][i % 4], a.scale, -c[n]);
+    if (!whole) {
+      vis = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (visible(a, t0 + 16 * (i / 4) + 4 * (int32_t)g + i % 4, pos[n]))
+          vis |= 1u << i;
+        else
+          p[i] = -INFINITY;
+      }
+    }
+    seen[n] |= vis != 0;
+    float top = p[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
+    if (__any(top > most[n])) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const bool fresh = most[n] == -INFINITY;
+      const float up = fresh ? (top == -INFINITY ? 0.f : top - kTop) : fmaxf(top - kTop, 0.f);
+      const float fade = fresh ? 1.f : __builtin_amdgcn_exp2f(-up);
+      c[n] += up;
+      if (top > -INFINITY) most[n] = kTop + kSlack;
+      l[n] *= fade;
+#pragma unroll
+      for (int d = 0; d < 2 * NB; ++d) o[n][d] *= fade;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = vis >> i & 1 ? fmaf(s[i / 4][n][i % 4], a.scale, -c[n]) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(p[i]);
+    return round8<F16>(p);
+  }
+
+  // Value blocks that are NaN, or past fp16's range: a weight of zero times such a value
+  // must not reach rows that do not see the token, so these blocks count as zeros, and the
+  // rows that see one become NaN in its dimensions.  A product of ones marks them.
+  static constexpr float kMostScale = F16 ? 0x1p13f : 0x1p127f;
+  __device__ __forceinline__ void mark_nan(Tile<NB>& t, float (&vs)[8], const uint32_t (&vis)[NQ]) {
     u32x4 is{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if ((t.vs[i / 4] >> 8 * (i % 4) & 255) != kScaleNaN) continue;
+      if (vs[i] <= kMostScale) continue;
       is[i / 2] |= 0x3f80u << 16 * (i % 2);
       clear_value(t, i / 4, i % 4);
+      vs[i] = 1.f;
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -373,15 +395,54 @@ struct Wave {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (vis[n] >> i & 1) see[i / 2] |= 0x3f80u << 16 * (i % 2);
-      const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, is),
-                                                                __builtin_bit_cast(bf16x8, see),
-                                                                f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+      const f32x4 hit = mfma16<false>(is, see, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-      for (int d = 0; d < 2 * NB; ++d)
+      for (int r = 0; r < 4; ++r) {
+        const float bad = hit[r] > 0.f ? __builtin_nanf("") : 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (hit[r] > 0.f) o[n][d][r] = __builtin_nanf("");
+        for (int d = 0; d < 2 * NB; ++d) o[n][d][r] += bad;
+      }
     }
+  }
+
+  // One tile of tokens from t0 on; whole: every row sees every token.
+  __device__ __forceinline__ void tile(const AttendArgs& a, Tile<NB>& t, int32_t t0, bool whole, int32_t stored,
+                                       uint32_t r16, uint32_t g) {
+    // tokens past the last one stored hold anything: as zeros they add nothing
+    if (t0 + 32 > stored) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (t0 + 16 * h + (int32_t)r16 >= stored) t.ks[h] = kScaleOne * 0x101u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t0 + 16 * h + 4 * (int32_t)g + i >= stored) clear_value(t, h, i);
+      }
+    }
+    f32x4 s[2][NQ];
+    u32x4 w[NQ];
+    uint32_t vis[NQ];
+    scores(t, s);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      w[n] = weights(a, s, n, t0, whole, g, vis[n]);
+      l[n] = mfma16<F16>(ones<F16>(), w[n], l[n]);
+    }
+    float vs[8], most_scale = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      vs[i] = scale_of(t.vs[i / 4] >> 8 * (i % 4) & 255);
+      most_scale = fmaxf(most_scale, vs[i]);
+    }
+    if (__any(most_scale > kMostScale)) mark_nan(t, vs, vis);
+    each<0, NB>([&](auto b) {
+      u32x4 even, odd;
+      value_operands<F16, NB, b.value>(t, vs, &even, &odd);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        o[n][2 * b.value] = mfma16<F16>(even, w[n], o[n][2 * b.value]);
+        o[n][2 * b.value + 1] = mfma16<F16>(odd, w[n], o[n][2 * b.value + 1]);
+      }
+    });
   }
 };
 
@@ -403,178 +464,220 @@ __device__ void none(const AttendArgs& a) {
   }
 }
 
-// A row's output: element e of NB * 2 tiles x 4 of the lane is dimension
-// 2 NB (4 g + e % 4) + e / 4.
+// How the parts of a row are joined: each part's factor is 2^(its offset - the largest),
+// parts that saw nothing or only scores of -inf aside.
+__device__ __forceinline__ bool has_weight(float sum) { return sum != kNothing && sum != 0.f; }
+
+template <bool F16>
+__device__ __forceinline__ void store_out(void* out, uint64_t at, f32x4 o, float l, bool seen) {
+  f32x4 y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = seen ? o[i] / l : 0.f;
+  u32x2 w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (F16)
+      w[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)y[2 * i], (_Float16)y[2 * i + 1]});
+    else
+      w[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)y[2 * i], (__bf16)y[2 * i + 1]});
+  }
+  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) = w;
+}
+
+// A row's output: element 4 d + r of the lane (o[n][d][r]) is dimension 2 NB (4 g + r) + d.
 template <int NB, int NQ, bool F16>
-__global__ void __launch_bounds__(256) k_kv4_attend(AttendArgs a) {
+__global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2) : NQ == 2 && NB < 8 ? 2 : 1) k_kv4_attend(AttendArgs a) {
   constexpr int D = 32 * NB;
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r16 = lane & 15, g = lane >> 4;
   const uint32_t b = blockIdx.z, head = blockIdx.y % a.c.heads, q_tile = blockIdx.y / a.c.heads;
   if (b == a.t.batch) {  // rows of no sequence
     none<D>(a);
     return;
   }
-  int32_t first = 0, n_rows = (int32_t)(a.t.rows / a.t.batch);
+  int32_t first, n_rows = (int32_t)(a.t.rows / a.t.batch);
   if (a.t.starts) {
     first = max(a.t.starts[b], 0);
     n_rows = max(min(a.t.starts[b + 1], (int32_t)a.t.rows), 0) - first;
   } else {
     first = (int32_t)b * n_rows;
   }
-  const int64_t all_rows = (int64_t)max(n_rows, 0) * a.group;
+  const uint32_t all_rows = (uint32_t)max(n_rows, 0) * a.group;  // the host keeps this under 2^31
   const int32_t len = a.t.lens[b];
-  __shared__ float sm[4][16 * NQ], sl[4][16 * NQ];
-  __shared__ float so[4][16][D + 4];
-  for (int64_t row0 = (int64_t)q_tile * (16 * NQ); row0 < all_rows; row0 += (int64_t)a.q_tiles * (16 * NQ)) {
-  const int64_t capacity = (int64_t)a.t.wide * a.c.page_tokens;
-  // positions of the tile's first and last rows
-  const int64_t last_row = min(row0 + 16 * NQ, all_rows) - 1;
-  const int64_t p_lo = (int64_t)len - n_rows + row0 / a.group, p_hi = (int64_t)len - n_rows + last_row / a.group;
-  const int64_t hi = min(p_hi, capacity - 1);
-  // tiles: those of the sinks, then from the window's first on
-  int32_t first_tile = 0, sink_tiles = 0, tiles = 0;
-  if (hi >= 0) {
-    if (a.window) first_tile = (int32_t)(max(p_lo - a.window + 1, (int64_t)0) / 32);
-    sink_tiles = min(min((a.sinks + 31) / 32, first_tile), (int32_t)(hi / 32) + 1);
-    tiles = max((int32_t)(hi / 32) - first_tile + 1, 0) + sink_tiles;
-  }
-  const uint32_t parts = a.splits * 4, part = blockIdx.x * 4 + wave;
-  const int32_t from = (int32_t)((int64_t)tiles * part / parts), to = (int32_t)((int64_t)tiles * (part + 1) / parts);
-
-  Wave<NB, NQ, F16> w;
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int64_t r = min(row0 + n * 16 + r16, all_rows - 1);
-    const uint32_t i = (uint32_t)(r / a.group), hq = head * a.group + (uint32_t)(r - (int64_t)i * a.group);
-    w.pos[n] = row0 + n * 16 + r16 < all_rows ? (int32_t)max((int64_t)len - n_rows + i, (int64_t)-1) : -1;
-    const uint16_t* q = a.q + (first + (int64_t)i) * a.q_row + hq * a.q_head;
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const u32x4 v = load_oct16(q, (g * NB + j) * 8, D, a.vec).v;
-      if constexpr (F16)
-        split_f16(v, &w.q[n][j], &w.ql[n][j]);
-      else
-        w.q[n][j] = __builtin_bit_cast(bf16x8, v);
-    }
-    w.m[n] = -INFINITY;
-    w.l[n] = 0.f;
-    w.seen[n] = false;
-#pragma unroll
-    for (int d = 0; d < 2 * NB; ++d) w.o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
+  const int32_t capacity = (int32_t)(a.t.wide * a.c.page_tokens);
+  const int32_t stored = min(len, capacity);
   const int32_t* table = a.t.table + b * a.t.stride;
-  for (int32_t v = from; v < to; ++v) {
-    const int32_t t0 = (v < sink_tiles ? v : v - sink_tiles + first_tile) * 32;
-    const uint32_t in_table = (uint32_t)t0 / a.c.page_tokens;
-    const int32_t page = table[in_table];
-    if (page < 0 || (uint32_t)page >= a.c.pages) continue;
-    Tile<NB> t;
-    load_tile<NB>(t, a.c.data + ((uint64_t)page * a.c.heads + head) * region_bytes(a.c), a.c.page_tokens,
-                  (uint32_t)t0 - in_table * a.c.page_tokens, r16, g);
-    const bool whole = t0 + 31 <= p_lo && row0 + 16 * NQ <= all_rows &&
-                       (a.window == 0 || t0 > p_hi - a.window || t0 + 32 <= a.sinks);
-    w.tile(a, t, t0, whole, (int32_t)min((int64_t)len, capacity), g);
-  }
+  __shared__ float sc[4][16 * NQ], sl[4][16 * NQ];
+  __shared__ uint32_t rows_at[16 * NQ];  // of the output
+  __shared__ __align__(16) float so[4][16][D + 4];
 
-  // the four waves' states joined through LDS
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float l = w.l[n];
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    uint32_t seen = w.seen[n];
-    seen |= (uint32_t)__shfl_xor((int)seen, 16);
-    seen |= (uint32_t)__shfl_xor((int)seen, 32);
-    if (g == 0) {
-      sm[wave][n * 16 + r16] = w.m[n];
-      sl[wave][n * 16 + r16] = seen ? l : kNothing;
+  for (uint32_t row0 = q_tile * (16 * NQ); row0 < all_rows; row0 += a.q_tiles * (16 * NQ)) {
+    // positions of the tile's first and last rows
+    const uint32_t last_row = min(row0 + 16 * NQ, all_rows) - 1;
+    const int64_t p_lo = (int64_t)len - n_rows + row0 / a.group, p_hi = (int64_t)len - n_rows + last_row / a.group;
+    const int32_t hi = (int32_t)min(max(p_hi, (int64_t)-1), (int64_t)capacity - 1);
+    // tiles: those of the sinks, then from the window's first on
+    int32_t first_tile = 0, sink_tiles = 0, tiles = 0;
+    if (hi >= 0) {
+      if (a.window) first_tile = (int32_t)(max(p_lo - a.window + 1, (int64_t)0) / 32);
+      sink_tiles = min(min((a.sinks + 31) / 32, first_tile), hi / 32 + 1);
+      tiles = max(hi / 32 - first_tile + 1, 0) + sink_tiles;
     }
-  }
-  const uint64_t all = (uint64_t)a.t.rows * a.q_heads;
-  for (int n = 0; n < NQ; ++n) {
-    __syncthreads();
+    // the block's tiles (the last split takes what is left), then the wave's
+    const uint32_t cut = blockIdx.x * a.chunk;
+    const int32_t from = (int32_t)min(cut, (uint32_t)tiles);
+    const int32_t count = blockIdx.x + 1 == a.splits ? tiles - from : min((int32_t)a.chunk, tiles - from);
+    int32_t v = from + (int32_t)((uint32_t)count * wave / 4);
+    const int32_t to = from + (int32_t)((uint32_t)count * (wave + 1) / 4);
+
+    // The next tile's loads are in flight while a tile is worked on, and the page after it
+    // is known by then.  A tile without a page, or none at all, loads page 0 and is passed
+    // over: loads on a condition would have the wave wait for all of them each time.
+    auto start_of = [&](int32_t i) { return (i < sink_tiles ? i : i - sink_tiles + first_tile) * 32; };
+    auto page_index = [&](int32_t t0) { return __umulhi((uint32_t)t0 / 32, a.per_page); };
+    auto page_of = [&](int32_t i) { return i < to ? table[page_index(start_of(i))] : -1; };
+    auto fetch = [&](Tile<NB>& t, int32_t i, int32_t page) {
+      const bool ok = (uint32_t)page < a.c.pages;
+      const uint32_t t0 = (uint32_t)start_of(i), in = t0 - page_index(t0) * a.c.page_tokens;
+      const uint64_t region = (ok ? (uint64_t)(uint32_t)page : 0) * a.c.heads + head;
+      load_tile<NB>(t, a.c.data + region * region_bytes(a.c), a.c.page_tokens, ok ? in : 0, r16, g);
+      return ok;
+    };
+    Tile<NB> t, next;
+    const int32_t page0 = page_of(v);
+    int32_t page1 = page_of(v + 1);
+    bool ok = fetch(t, v, page0);
+
+    Wave<NB, NQ, F16> w;
 #pragma unroll
-    for (int nn = 0; nn < NQ; ++nn)
-      if (nn == n) {
+    for (int n = 0; n < NQ; ++n) {
+      const uint32_t r = min(row0 + n * 16 + r16, all_rows - 1), i = r / a.group, hq = head * a.group + (r - i * a.group);
+      const bool real = row0 + n * 16 + r16 < all_rows;
+      w.pos[n] = real ? (int32_t)max((int64_t)len - n_rows + i, (int64_t)-1) : -1;
+      const uint16_t* q = a.q + (first + (int64_t)i) * a.q_row + hq * a.q_head + g * (8 * NB);
+      if (a.vec) {
 #pragma unroll
-        for (int d = 0; d < 2 * NB; ++d)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) so[wave][r16][2 * NB * (4 * g + r) + d] = w.o[nn][d][r];
-      }
-    __syncthreads();
-    for (uint32_t e = threadIdx.x; e < 16 * D; e += 256) {
-      const uint32_t row = e / D, d = e % D;
-      const int64_t r = row0 + n * 16 + row;
-      if (r >= all_rows) continue;
-      float m = -INFINITY, l = 0.f, o = 0.f;
-      bool seen = false;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (sl[v][n * 16 + row] == kNothing) continue;
-        seen = true;
-        m = fmaxf(m, sm[v][n * 16 + row]);
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (sl[v][n * 16 + row] == kNothing) continue;
-        const float f = __builtin_amdgcn_exp2f(sm[v][n * 16 + row] - base);
-        l += f * sl[v][n * 16 + row];
-        o += f * so[v][row][d];
-      }
-      const uint32_t i = (uint32_t)(r / a.group);
-      const uint64_t at = (first + (uint64_t)i) * a.q_heads + head * a.group + (uint32_t)(r - (int64_t)i * a.group);
-      if (a.splits == 1) {
-        const float y = seen ? o / l : 0.f;
-        if constexpr (F16)
-          static_cast<_Float16*>(a.o)[at * D + d] = (_Float16)y;
-        else
-          static_cast<__bf16*>(a.o)[at * D + d] = (__bf16)y;
+        for (int j = 0; j < NB; ++j) w.q[n][j] = reinterpret_cast<const u32x4*>(q)[j];
       } else {
-        a.part[(blockIdx.x * all + at) * D + d] = o;
-        if (d == 0) {
-          float* ml = a.part + a.splits * all * D + (blockIdx.x * all + at) * 2;
-          ml[0] = m;
-          ml[1] = seen ? l : kNothing;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) w.q[n][j] = load_oct16(q, j * 8, D, false).v;
+      }
+      if (wave == 0 && g == 0) rows_at[n * 16 + r16] = real ? (first + i) * a.q_heads + hq : ~0u;
+      w.c[n] = 0.f;
+      w.most[n] = -INFINITY;
+      w.seen[n] = false;
+      w.l[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < 2 * NB; ++d) w.o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    for (; v < to; ++v) {
+      const int32_t page2 = page_of(v + 2);
+      const bool ok1 = fetch(next, v + 1, page1);
+      const int32_t t0 = start_of(v);
+      const bool whole = t0 + 31 <= p_lo && row0 + 16 * NQ <= all_rows &&
+                         (a.window == 0 || t0 > p_hi - a.window || t0 + 32 <= a.sinks);
+      if (ok) w.tile(a, t, t0, whole, stored, r16, g);
+      t = next;
+      ok = ok1;
+      page1 = page2;
+    }
+
+    // the four waves' states joined through LDS
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      uint32_t seen = w.seen[n];
+      seen |= (uint32_t)__shfl_xor((int)seen, 16);
+      seen |= (uint32_t)__shfl_xor((int)seen, 32);
+      if (g == 0) {
+        sc[wave][n * 16 + r16] = w.c[n];
+        sl[wave][n * 16 + r16] = seen ? w.l[n][0] : kNothing;
+      }
+    }
+    const uint64_t all = (uint64_t)a.t.rows * a.q_heads;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      if (row0 + n * 16 >= all_rows) break;
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < 2 * NB; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) so[wave][r16][2 * NB * (4 * g + r) + d] = w.o[n][d][r];
+      __syncthreads();
+      for (uint32_t e = threadIdx.x; e < 16 * D / 4; e += 256) {
+        const uint32_t row = e / (D / 4), d = e % (D / 4) * 4;
+        const uint64_t at = rows_at[n * 16 + row];
+        if (at == ~0u) continue;
+        float c = -INFINITY, l = 0.f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        bool seen = false;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          seen |= sl[v][n * 16 + row] != kNothing;
+          if (has_weight(sl[v][n * 16 + row])) c = fmaxf(c, sc[v][n * 16 + row]);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (!has_weight(sl[v][n * 16 + row])) continue;
+          const float f = __builtin_amdgcn_exp2f(sc[v][n * 16 + row] - c);
+          l += f * sl[v][n * 16 + row];
+          o += f * *reinterpret_cast<const f32x4*>(&so[v][row][d]);
+        }
+        if (a.splits == 1) {
+          store_out<F16>(a.o, at * D + d, o, l, seen);
+        } else {
+          *reinterpret_cast<f32x4*>(a.part + (blockIdx.x * all + at) * D + d) = o;
+          if (d == 0)
+            *reinterpret_cast<f32x2*>(a.part + a.splits * all * D + (blockIdx.x * all + at) * 2) =
+                f32x2{c, seen ? l : kNothing};
         }
       }
     }
-  }
-  __syncthreads();
+    __syncthreads();
   }
 }
 
-// The splits of a row joined, in their order.
+// The splits of a row joined, in their order: a wave per row, lane s first holding split
+// s's factor, then D / 64 dimensions.
+constexpr uint32_t kMostSplits = 64;
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) k_kv4_join(const float* __restrict__ part, void* __restrict__ out, uint64_t all,
                                                   uint32_t splits) {
-  const uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x, at = e / D;
+  constexpr int N = D / 64;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t at = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (at >= all) return;
-  const float* ml = part + splits * all * D;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  bool seen = false;
+  const float* cl = part + splits * all * D + at * 2;
+  const f32x2 mine = lane < splits ? *reinterpret_cast<const f32x2*>(cl + lane * all * 2) : f32x2{0.f, kNothing};
+  const bool some = has_weight(mine[1]);
+  float c = some ? mine[0] : -INFINITY;
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) c = fmaxf(c, __shfl_xor(c, i));
+  const float f = some ? __builtin_amdgcn_exp2f(mine[0] - c) : 0.f;
+  float l = some ? f * mine[1] : 0.f;
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) l += __shfl_xor(l, i);
+  const bool seen = __any(mine[1] != kNothing);
+  float o[N] = {};
+#pragma unroll 8
   for (uint32_t s = 0; s < splits; ++s) {
-    if (ml[(s * all + at) * 2 + 1] == kNothing) continue;
-    seen = true;
-    m = fmaxf(m, ml[(s * all + at) * 2]);
+    const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+    const float* p = part + (s * all + at) * D + lane * N;
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = fs != 0.f ? fmaf(fs, x[i], o[i]) : o[i];  // a part of no weight may be unwritten
   }
-  const float base = m == -INFINITY ? 0.f : m;
-  for (uint32_t s = 0; s < splits; ++s) {
-    const float ls = ml[(s * all + at) * 2 + 1];
-    if (ls == kNothing) continue;
-    const float f = __builtin_amdgcn_exp2f(ml[(s * all + at) * 2] - base);
-    l += f * ls;
-    o += f * part[s * all * D + e];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float y = seen ? o[i] / l : 0.f;
+    if constexpr (F16)
+      static_cast<_Float16*>(out)[at * D + lane * N + i] = (_Float16)y;
+    else
+      static_cast<__bf16*>(out)[at * D + lane * N + i] = (__bf16)y;
   }
-  const float y = seen ? o / l : 0.f;
-  if constexpr (F16)
-    static_cast<_Float16*>(out)[e] = (_Float16)y;
-  else
-    static_cast<__bf16*>(out)[e] = (__bf16)y;
 }
-
 
 }  // namespace ecw
 
@@ -624,10 +727,13 @@ bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
   return n >> 31 == 0;
 }
 
+constexpr uint64_t kBlocks = 2048;  // blocks that an attention call is split into at most
+constexpr uint64_t kChunk = 8;      // tiles of 32 tokens of a split at least, for its four waves
+
 // How an attention call is cut up: query tiles of 16 nq rows, and splits of each
 // sequence's tokens.
 struct Plan {
-  uint32_t nq, q_tiles, splits;
+  uint32_t nq, q_tiles, splits, chunk;
 };
 
 Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
@@ -635,7 +741,7 @@ Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* a
   const uint64_t group = at->q_heads / c->kv_heads;
   const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;
   const uint64_t rows = each * group;
-  p.nq = rows <= 16 ? 1 : 2;
+  p.nq = rows <= 16 ? 1 : rows <= 32 || c->head_dim == 256 ? 2 : 4;
   uint64_t tiles_q = (rows + 16 * p.nq - 1) / (16 * p.nq);
   const uint64_t most = 65535 / c->kv_heads;
   p.q_tiles = (uint32_t)(tiles_q < most ? tiles_q : most);
@@ -645,12 +751,14 @@ Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* a
     const uint64_t seen = (uint64_t)at->window + at->sinks + each;
     if (seen < len) len = seen;
   }
-  const uint64_t tiles = (len + 31) / 32, blocks = (uint64_t)p.q_tiles * c->kv_heads * r->batch;
-  uint64_t splits = (1024 + blocks - 1) / blocks;
-  const uint64_t top = (tiles + 7) / 8;  // two tiles a wave at least
+  const uint64_t tiles = (len + 31) / 32 + 1, blocks = (uint64_t)p.q_tiles * c->kv_heads * r->batch;
+  uint64_t splits = kBlocks / blocks;
+  const uint64_t top = (tiles + kChunk - 1) / kChunk;
   if (splits > top) splits = top;
-  if (splits > 64) splits = 64;
-  p.splits = splits ? (uint32_t)splits : 1;
+  if (splits > kMostSplits) splits = kMostSplits;
+  if (splits < 1) splits = 1;
+  p.chunk = (uint32_t)((tiles + splits - 1) / splits);
+  p.splits = (uint32_t)((tiles + p.chunk - 1) / p.chunk);
   return p;
 }
 
@@ -659,6 +767,8 @@ ecw_status check_attention(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv
   if (!at) return refuse(ECW_E_INVALID_ARG, "attention is NULL");
   if (at->q_heads == 0 || at->q_heads % c->kv_heads || at->q_heads > 65536)
     return refuse(ECW_E_INVALID_ARG, "q_heads must be a positive multiple of kv_heads, at most 65536");
+  if ((uint64_t)r->rows * at->q_heads >> 31)
+    return refuse(ECW_E_UNSUPPORTED, "rows times q_heads must be below 2^31");
   if (at->window > 1u << 30 || at->sinks > 1u << 30)
     return refuse(ECW_E_INVALID_ARG, "window and sinks must be at most 2^30");
   if (!(at->scale - at->scale == 0.f)) return refuse(ECW_E_INVALID_ARG, "scale must be finite");
@@ -679,11 +789,13 @@ template <int NB, bool F16>
 ecw_status launch_all(hipStream_t stream, const AttendArgs& a, uint32_t nq) {
   if (nq == 1)
     launch_attend<NB, 1, F16>(stream, a);
-  else
+  else if (nq == 2 || NB == 8)
     launch_attend<NB, 2, F16>(stream, a);
+  else
+    launch_attend<NB, NB == 8 ? 2 : 4, F16>(stream, a);
   if (ecw_status s = launched("kv4_attend")) return s;
   if (a.splits == 1) return ECW_OK;
-  const uint64_t all = (uint64_t)a.t.rows * a.q_heads, grid = (all * (32 * NB) + 255) / 256;
+  const uint64_t all = (uint64_t)a.t.rows * a.q_heads, grid = (all + 3) / 4;
   hipLaunchKernelGGL((k_kv4_join<32 * NB, F16>), dim3((uint32_t)grid), dim3(256), 0, stream, a.part, a.o, all,
                      a.splits);
   return launched("kv4_attend");
@@ -768,8 +880,6 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
   const Plan p = plan_of(cache, rows, at);
   if (part_bytes(cache, rows, at, p) > workspace_bytes || (p.splits > 1 && (!workspace || !aligned(workspace, 16))))
     return refuse(ECW_E_INVALID_ARG, "workspace missing, too small or not 16-byte aligned");
-  if (((uint64_t)rows->rows * at->q_heads * cache->head_dim + 255) / 256 >> 31)
-    return refuse(ECW_E_UNSUPPORTED, "too many rows for one launch");
   AttendArgs a{};
   a.c = cache_of(cache);
   a.t = batch_of(rows);
@@ -782,6 +892,9 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
   a.q_heads = at->q_heads;
   a.q_tiles = p.q_tiles;
   a.splits = p.splits;
+  a.chunk = p.chunk;
+  const uint32_t page_tiles = cache->page_tokens / 32;
+  a.per_page = (uint32_t)(((uint64_t(1) << 32) + page_tiles - 1) / page_tiles);
   a.window = (int32_t)at->window;
   a.sinks = (int32_t)at->sinks;
   a.scale = at->scale * 1.44269504088896f;

@@ -66,9 +66,7 @@ def _lib():
     return _bound
 
 
-def _here(device, stream) -> bool:
-    """Whether the call can run as it stands: current device, current stream."""
-    return stream is None and device.index == torch.cuda.current_device()
+_get_device = torch._C._cuda_getDevice
 
 
 def _elsewhere(device, stream, tensors, call):
@@ -82,26 +80,29 @@ def _elsewhere(device, stream, tensors, call):
 
 
 def _on_gpu(t, name):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a cuda tensor")
 
 
 def _float(t, name, dtypes=_FLOATS):
-    if t.dtype not in dtypes:
+    d = dtypes.get(t.dtype)
+    if d is None:
         raise TypeError(f"{name} must be " + ", ".join(str(d).replace("torch.", "") for d in dtypes))
-    return _FLOATS[t.dtype]
+    return d
 
 
 _HALVES = {torch.float16: DT_F16, torch.bfloat16: DT_BF16}
 
 
-def _ints(t, name, device, shape):
+def _bad_ints(t, name, device, shape):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
         raise TypeError(f"{name} must be an int32 tensor on {device}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if s is None else s for s in shape)}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise TypeError(f"{name} must have a unit inner stride")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    raise TypeError(f"{name} must have a unit inner stride")
+
+
+_I32 = torch.int32
 
 
 class MX4Tensor:
@@ -137,7 +138,7 @@ class MX4Tensor:
     def dequantize(self, dtype=torch.float16, out=None, stream=None) -> torch.Tensor:
         """The values as a dense [rows, cols] matrix: exact in bfloat16 and float32."""
         dev = self.codes.device
-        if not _here(dev, stream):
+        if stream is not None or dev.index != _get_device():
             return _elsewhere(dev, stream, (self.codes, self.scales, out), lambda: self.dequantize(dtype, out))
         if out is None:
             out = torch.empty((self.rows, self.cols), dtype=dtype, device=dev)
@@ -152,18 +153,20 @@ class MX4Tensor:
         [batch, cols]; y [batch, rows], fp32 unless out_dtype (fp16, bf16) says otherwise."""
         dev = self.codes.device
         both = isinstance(x, MX4Tensor)
-        if not both:
+        if both:
+            batch, cols = x.rows, x.cols
+        else:
             _on_gpu(x, "x")
             if x.dim() == 1:
                 x = x.unsqueeze(0)
             if x.dim() != 2:
                 raise ValueError("x must be [batch, cols]")
-        batch, cols = x.shape
+            batch, cols = x.shape
         if cols != self.cols:
             raise ValueError(f"x has {cols} columns, the tensor {self.cols}")
         if x.device != dev:
             raise ValueError(f"x is on {x.device}, the tensor on {dev}")
-        if not _here(dev, stream):
+        if stream is not None or dev.index != _get_device():
             used = (x.codes, x.scales) if both else (x,)
             return _elsewhere(dev, stream, (self.codes, self.scales, y, *used), lambda: self.gemm(x, y, out_dtype))
         if y is None:
@@ -196,7 +199,7 @@ def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None, stream=None) -> 
     if cols > 1 and x.stride(1) != 1:
         raise TypeError("x must have a unit inner stride")
     dev = x.device
-    if not _here(dev, stream):
+    if stream is not None or dev.index != _get_device():
         used = (x,) if out is None else (x, out.codes, out.scales)
         return _elsewhere(dev, stream, used, lambda: mx4_quantize(x, out))
     if out is None:
@@ -231,23 +234,35 @@ class KV4Cache:
         _on_gpu(self.data, "cache")
         self._c.data = self.data.data_ptr()
         self.pages, self.kv_heads, self.head_dim, self.page_tokens = pages, kv_heads, head_dim, page_tokens
+        self.device = self.data.device
+        self._plans = {}
 
     def _rows(self, page_table, lens, starts, rows):
-        dev = self.data.device
-        _ints(page_table, "page_table", dev, (None, None))
+        dev = self.device
+        if (not isinstance(page_table, torch.Tensor) or page_table.dtype is not _I32 or page_table.device != dev
+                or page_table.dim() != 2):
+            _bad_ints(page_table, "page_table", dev, ("batch", "width"))
         batch, width = page_table.shape
-        _ints(lens, "lens", dev, (batch,))
+        stride, inner = page_table.stride()
+        if inner != 1 and width > 1 and batch:
+            _bad_ints(page_table, "page_table", dev, (batch, width))
+        if (not isinstance(lens, torch.Tensor) or lens.dtype is not _I32 or lens.device != dev
+                or lens.shape != (batch,) or not lens.is_contiguous()):
+            _bad_ints(lens, "lens", dev, (batch,))
+        first = None
         if starts is not None:
-            _ints(starts, "starts", dev, (batch + 1,))
+            if (not isinstance(starts, torch.Tensor) or starts.dtype is not _I32 or starts.device != dev
+                    or starts.shape != (batch + 1,) or not starts.is_contiguous()):
+                _bad_ints(starts, "starts", dev, (batch + 1,))
+            first = starts.data_ptr()
         elif rows and (batch == 0 or rows % batch):
             raise ValueError(f"{rows} rows are not the same number for each of {batch} sequences: pass starts")
-        return _Rows(page_table.data_ptr(), page_table.stride(0), lens.data_ptr(),
-                     starts.data_ptr() if starts is not None else None, batch, width, rows)
+        return _Rows(page_table.data_ptr(), stride, lens.data_ptr(), first, batch, width, rows)
 
     def _heads(self, t, name, heads=None):
-        _on_gpu(t, name)
-        if t.device != self.data.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {self.data.device}")
+        if not isinstance(t, torch.Tensor) or t.device != self.device:
+            _on_gpu(t, name)
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         if t.dim() != 3 or t.shape[2] != self.head_dim or (heads and t.shape[1] != heads):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (*, {heads or '*'}, {self.head_dim})")
         if t.stride(2) != 1:
@@ -261,9 +276,9 @@ class KV4Cache:
         if k.shape[0] != v.shape[0] or k.dtype != v.dtype:
             raise ValueError("k and v must agree in rows and dtype")
         dt = _float(k, "k")
-        dev = self.data.device
+        dev = self.device
         r = self._rows(page_table, lens, starts, k.shape[0])
-        if not _here(dev, stream):
+        if stream is not None or dev.index != _get_device():
             return _elsewhere(dev, stream, (self.data, k, v, page_table, lens, starts),
                               lambda: self.append(k, v, page_table, lens, starts))
         strides = (ctypes.c_int64 * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
@@ -275,9 +290,9 @@ class KV4Cache:
         zeros for a row without a page."""
         if rows < 0:
             raise ValueError("rows must not be negative")
-        dev = self.data.device
+        dev = self.device
         r = self._rows(page_table, lens, starts, rows)
-        if not _here(dev, stream):
+        if stream is not None or dev.index != _get_device():
             return _elsewhere(dev, stream, (self.data, page_table, lens, starts),
                               lambda: self.read(page_table, lens, rows, starts, dtype))
         k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=dtype, device=dev)
@@ -302,9 +317,9 @@ class KV4Cache:
             raise ValueError(f"{q_heads} query heads are no multiple of {self.kv_heads} key/value heads")
         if window < 0 or sinks < 0 or (max_rows or 0) < 0 or (max_len or 0) < 0:
             raise ValueError("window, sinks, max_rows and max_len must not be negative")
-        dev = self.data.device
+        dev = self.device
         r = self._rows(page_table, lens, starts, rows)
-        if not _here(dev, stream):
+        if stream is not None or dev.index != _get_device():
             return _elsewhere(dev, stream, (self.data, q, page_table, lens, starts, out),
                               lambda: self.attend(q, page_table, lens, starts, max_rows, max_len, window, sinks,
                                                   scale, out))
@@ -312,13 +327,21 @@ class KV4Cache:
             out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=dev)
         elif tuple(out.shape) != tuple(q.shape) or not out.is_contiguous() or out.dtype != q.dtype or out.device != dev:
             raise ValueError(f"out must be a contiguous {tuple(q.shape)} {q.dtype} tensor on {dev}")
-        top = (1 << 30)
-        a = _Attention(q_heads, min(max_rows or 0, top), min(max_len or 0, top), min(window, top), min(sinks, top),
-                       dim ** -0.5 if scale is None else scale)
         L = _lib()
-        n = ctypes.c_size_t(0)
-        _check(L.kv4_attend_workspace_size(self._c, r, a, n), "kv4_attend_workspace_size")
-        ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+        # the attention's description and workspace by its sizes, which a decode loop repeats
+        key = (rows, q_heads, r.batch, r.table_width, max_rows, max_len, window, sinks, scale)
+        plan = self._plans.get(key)
+        if plan is None:
+            top = 1 << 30
+            a = _Attention(q_heads, min(max_rows or 0, top), min(max_len or 0, top), min(window, top),
+                           min(sinks, top), dim ** -0.5 if scale is None else scale)
+            n = ctypes.c_size_t(0)
+            _check(L.kv4_attend_workspace_size(self._c, r, a, n), "kv4_attend_workspace_size")
+            if len(self._plans) >= 64:
+                self._plans.clear()
+            plan = self._plans[key] = a, n.value
+        a, n = plan
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         _check(L.kv4_attend(_raw_stream(dev.index), self._c, r, a, q.data_ptr(), dt, q.stride(0), q.stride(1),
-                            out.data_ptr(), ws.data_ptr() if ws is not None else None, n.value), "kv4_attend")
+                            out.data_ptr(), ws.data_ptr() if n else None, n), "kv4_attend")
         return out

@@ -66,7 +66,7 @@ class Bed:
             p = table[b][np.arange(n) // page]
             self.there.append((p >= 0) & (p < pages))
 
-    def check(self, o, q, rows, window=0, sinks=0, scale=None, lens=None, skip=()):
+    def check(self, o, q, rows, window=0, sinks=0, scale=None, lens=None, skip=(), grid=1e-30):
         """rows: how many of each sequence, in order."""
         scale = self.dim ** -0.5 if scale is None else scale
         half = {BF16: 2.0 ** -8, FP16: 2.0 ** -11}[o.dtype]
@@ -77,7 +77,7 @@ class Bed:
                                            R.rounded(F64(self.v[b])), self.there[b], scale, window, sinks)
             score = (self.dim / 32 + 64) * 2.0 ** -23 * dot + 2.0 ** -18
             tol = (2.0 ** -8 + 2 * score + (len(self.k[b]) / 32 + 128) * 2.0 ** -23) * mag
-            tol = tol + half * (np.abs(want) + tol) + 1e-30
+            tol = tol + half * (np.abs(want) + tol) + grid
             mine = got[at:at + n]
             if b not in skip:
                 nan = np.isnan(want)
@@ -239,6 +239,26 @@ def test_nan_and_infinity_reach_only_rows_that_see_them(dim, n):
     q = _normal(92, n, 4, dim)
     bed.check(bed.cache.attend(q, bed.table, I32([400]), window=100), q, [n], 100)
     bed.check(bed.cache.attend(q, bed.table, I32([400])), q, [n])
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_fp16_queries_over_values_of_other_types(n):
+    """Small values round to fp16's grid (by 2^-25 at most); values past its range are NaN
+    to the rows that see them, and to no other."""
+    _say("attend fp16 range", n)
+    k, v = [_normal(1, 200, 1, 64)], [_normal(2, 200, 1, 64)]
+    v[0][:, :, :32] *= 2.0 ** -30
+    k[0][50:60, :, 32:] *= 2.0 ** -28
+    bed = Bed([200], 1, 64, k=k, v=v)
+    q = _normal(92, n, 2, 64, dtype=FP16)
+    o = bed.cache.attend(q, bed.table, I32([200]))
+    bed.check(o, q, [n], grid=2.0 ** -24)  # the values' and the output's
+    v[0][190, 0, 3] = 1e6
+    bed = Bed([200], 1, 64, k=k, v=v)
+    o = bed.cache.attend(q, bed.table, I32([200]))
+    sees = torch.arange(200 - n, 200) >= 190
+    assert bool(torch.isnan(o[sees][..., :32]).all()) and bool(torch.isfinite(o[sees][..., 32:]).all())
+    assert bool(torch.isfinite(o[~sees]).all())
 
 
 def test_peaked_and_equal_scores():
