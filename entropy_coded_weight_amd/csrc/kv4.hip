@@ -454,7 +454,7 @@ __device__ void none(const AttendArgs& a) {
   const uint32_t hi = min((uint32_t)max(a.t.starts[a.t.batch], (int32_t)lo), a.t.rows);
   const uint64_t all = (uint64_t)a.t.rows * a.q_heads, before = (uint64_t)lo * a.q_heads;
   const uint64_t nobody = before + (uint64_t)(a.t.rows - hi) * a.q_heads;
-  for (uint64_t e = threadIdx.x; e < nobody; e += 256) {
+  for (uint64_t e = threadIdx.x; e < nobody; e += blockDim.x) {
     const uint64_t at = e < before ? e : e - before + (uint64_t)hi * a.q_heads;
     if (a.splits > 1) {
       a.part[a.splits * all * D + (blockIdx.x * all + at) * 2 + 1] = kNothing;
@@ -484,11 +484,15 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, f32x4 o, float
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
+// The most waves of a block: what a CU's registers hold.
+constexpr uint32_t most_waves(int nb, int nq) { return 4 * (nq == 1 ? (nb == 2 ? 4 : nb == 4 ? 3 : 2) : nb < 8 ? 2 : 1); }
+
 // A row's output: element 4 d + r of the lane (o[n][d][r]) is dimension 2 NB (4 g + r) + d.
 template <int NB, int NQ, bool F16>
-__global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2) : NQ == 2 && NB < 8 ? 2 : 1) k_kv4_attend(AttendArgs a) {
-  constexpr int D = 32 * NB;
+__global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendArgs a) {
+  constexpr int D = 32 * NB, kWaves = most_waves(NB, NQ);
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t waves = blockDim.x >> 6;
   const uint32_t r16 = lane & 15, g = lane >> 4;
   const uint32_t b = blockIdx.z, head = blockIdx.y % a.c.heads, q_tile = blockIdx.y / a.c.heads;
   if (b == a.t.batch) {  // rows of no sequence
@@ -507,9 +511,9 @@ __global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2)
   const int32_t capacity = (int32_t)(a.t.wide * a.c.page_tokens);
   const int32_t stored = min(len, capacity);
   const int32_t* table = a.t.table + b * a.t.stride;
-  __shared__ float sc[4][16 * NQ], sl[4][16 * NQ];
+  __shared__ float sc[kWaves][16 * NQ], sl[kWaves][16 * NQ];
   __shared__ uint32_t rows_at[16 * NQ];  // of the output
-  __shared__ __align__(16) float so[4][16][D + 4];
+  __shared__ __align__(16) float so[kWaves][4][D + 4];
 
   for (uint32_t row0 = q_tile * (16 * NQ); row0 < all_rows; row0 += a.q_tiles * (16 * NQ)) {
     // positions of the tile's first and last rows
@@ -523,12 +527,10 @@ __global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2)
       sink_tiles = min(min((a.sinks + 31) / 32, first_tile), hi / 32 + 1);
       tiles = max(hi / 32 - first_tile + 1, 0) + sink_tiles;
     }
-    // the block's tiles (the last split takes what is left), then the wave's
-    const uint32_t cut = blockIdx.x * a.chunk;
-    const int32_t from = (int32_t)min(cut, (uint32_t)tiles);
-    const int32_t count = blockIdx.x + 1 == a.splits ? tiles - from : min((int32_t)a.chunk, tiles - from);
-    int32_t v = from + (int32_t)((uint32_t)count * wave / 4);
-    const int32_t to = from + (int32_t)((uint32_t)count * (wave + 1) / 4);
+    // the block's tiles (the last split takes what is left), which its waves take in turn
+    const int32_t cut = (int32_t)(blockIdx.x * a.chunk), step = (int32_t)waves;
+    const int32_t to = blockIdx.x + 1 == a.splits ? tiles : min(cut + (int32_t)a.chunk, tiles);
+    int32_t v = cut + (int32_t)wave;
 
     // The next tile's loads are in flight while a tile is worked on, and the page after it
     // is known by then.  A tile without a page, or none at all, loads page 0 and is passed
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2)
     };
     Tile<NB> t, next;
     const int32_t page0 = page_of(v);
-    int32_t page1 = page_of(v + 1);
+    int32_t page1 = page_of(v + step);
     bool ok = fetch(t, v, page0);
 
     Wave<NB, NQ, F16> w;
@@ -571,9 +573,9 @@ __global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2)
       for (int d = 0; d < 2 * NB; ++d) w.o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    for (; v < to; ++v) {
-      const int32_t page2 = page_of(v + 2);
-      const bool ok1 = fetch(next, v + 1, page1);
+    for (; v < to; v += step) {
+      const int32_t page2 = page_of(v + 2 * step);
+      const bool ok1 = fetch(next, v + step, page1);
       const int32_t t0 = start_of(v);
       const bool whole = t0 + 31 <= p_lo && row0 + 16 * NQ <= all_rows &&
                          (a.window == 0 || t0 > p_hi - a.window || t0 + 32 <= a.sinks);
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2)
       page1 = page2;
     }
 
-    // the four waves' states joined through LDS
+    // the waves' states joined through LDS, four rows at a time
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       uint32_t seen = w.seen[n];
@@ -596,43 +598,49 @@ __global__ void __launch_bounds__(256, NQ == 1 ? (NB == 2 ? 4 : NB == 4 ? 3 : 2)
     }
     const uint64_t all = (uint64_t)a.t.rows * a.q_heads;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      if (row0 + n * 16 >= all_rows) break;
-      __syncthreads();
+    for (int n = 0; n < NQ; ++n)
+      for (uint32_t r4 = 0; r4 < 16 && row0 + n * 16 + r4 < all_rows; r4 += 4) {
+        __syncthreads();
+        if ((r16 & ~3u) == r4) {
 #pragma unroll
-      for (int d = 0; d < 2 * NB; ++d)
+          for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) so[wave][r16][2 * NB * (4 * g + r) + d] = w.o[n][d][r];
-      __syncthreads();
-      for (uint32_t e = threadIdx.x; e < 16 * D / 4; e += 256) {
-        const uint32_t row = e / (D / 4), d = e % (D / 4) * 4;
-        const uint64_t at = rows_at[n * 16 + row];
-        if (at == ~0u) continue;
-        float c = -INFINITY, l = 0.f;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        bool seen = false;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          seen |= sl[v][n * 16 + row] != kNothing;
-          if (has_weight(sl[v][n * 16 + row])) c = fmaxf(c, sc[v][n * 16 + row]);
+            for (int d = 0; d < 2 * NB; ++d) so[wave][r16 & 3][2 * NB * (4 * g + r) + d] = w.o[n][d][r];
         }
+        __syncthreads();
+        for (uint32_t e = threadIdx.x; e < D; e += blockDim.x) {
+          const uint32_t row = e / (D / 4), d = e % (D / 4) * 4, in = n * 16 + r4 + row;
+          const uint64_t at = rows_at[in];
+          if (at == ~0u) continue;
+          float c = -INFINITY, l = 0.f;
+          f32x4 o = {0.f, 0.f, 0.f, 0.f};
+          bool seen = false;
+          for (uint32_t v4 = 0; v4 < waves; v4 += 4) {  // four at a time: their reads run together
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if (!has_weight(sl[v][n * 16 + row])) continue;
-          const float f = __builtin_amdgcn_exp2f(sc[v][n * 16 + row] - c);
-          l += f * sl[v][n * 16 + row];
-          o += f * *reinterpret_cast<const f32x4*>(&so[v][row][d]);
-        }
-        if (a.splits == 1) {
-          store_out<F16>(a.o, at * D + d, o, l, seen);
-        } else {
-          *reinterpret_cast<f32x4*>(a.part + (blockIdx.x * all + at) * D + d) = o;
-          if (d == 0)
-            *reinterpret_cast<f32x2*>(a.part + a.splits * all * D + (blockIdx.x * all + at) * 2) =
-                f32x2{c, seen ? l : kNothing};
+            for (uint32_t v = v4; v < v4 + 4; ++v) {
+              seen |= sl[v][in] != kNothing;
+              c = fmaxf(c, has_weight(sl[v][in]) ? sc[v][in] : -INFINITY);
+            }
+          }
+          for (uint32_t v4 = 0; v4 < waves; v4 += 4) {
+#pragma unroll
+            for (uint32_t v = v4; v < v4 + 4; ++v) {
+              const bool some = has_weight(sl[v][in]);
+              const float f = some ? __builtin_amdgcn_exp2f(sc[v][in] - c) : 0.f;
+              l += some ? f * sl[v][in] : 0.f;
+              o += f * *reinterpret_cast<const f32x4*>(&so[v][row][d]);  // zero where there is no weight
+            }
+          }
+          if (a.splits == 1) {
+            store_out<F16>(a.o, at * D + d, o, l, seen);
+          } else {
+            *reinterpret_cast<f32x4*>(a.part + (blockIdx.x * all + at) * D + d) = o;
+            if (d == 0)
+              *reinterpret_cast<f32x2*>(a.part + a.splits * all * D + (blockIdx.x * all + at) * 2) =
+                  f32x2{c, seen ? l : kNothing};
+          }
         }
       }
-    }
     __syncthreads();
   }
 }
@@ -727,13 +735,13 @@ bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
   return n >> 31 == 0;
 }
 
-constexpr uint64_t kBlocks = 2048;  // blocks that an attention call is split into at most
-constexpr uint64_t kChunk = 8;      // tiles of 32 tokens of a split at least, for its four waves
+constexpr uint64_t kChunk = 8;   // tiles of 32 tokens of a split at least, for its four waves
+constexpr uint64_t kAlone = 1;   // tiles a wave up to which one block takes a sequence
 
 // How an attention call is cut up: query tiles of 16 nq rows, and splits of each
 // sequence's tokens.
 struct Plan {
-  uint32_t nq, q_tiles, splits, chunk;
+  uint32_t nq, q_tiles, waves, splits, chunk;
 };
 
 Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
@@ -741,7 +749,7 @@ Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* a
   const uint64_t group = at->q_heads / c->kv_heads;
   const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;
   const uint64_t rows = each * group;
-  p.nq = rows <= 16 ? 1 : rows <= 32 || c->head_dim == 256 ? 2 : 4;
+  p.nq = rows <= 16 ? 1 : 2;  // four take all registers: 275 us for 512 rows behind 16384 tokens, two 216
   uint64_t tiles_q = (rows + 16 * p.nq - 1) / (16 * p.nq);
   const uint64_t most = 65535 / c->kv_heads;
   p.q_tiles = (uint32_t)(tiles_q < most ? tiles_q : most);
@@ -752,11 +760,19 @@ Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* a
     if (seen < len) len = seen;
   }
   const uint64_t tiles = (len + 31) / 32 + 1, blocks = (uint64_t)p.q_tiles * c->kv_heads * r->batch;
-  uint64_t splits = kBlocks / blocks;
-  const uint64_t top = (tiles + kChunk - 1) / kChunk;
-  if (splits > top) splits = top;
-  if (splits > kMostSplits) splits = kMostSplits;
-  if (splits < 1) splits = 1;
+  const uint32_t most_w = most_waves((int)c->head_dim / 32, (int)p.nq);
+  uint64_t splits = 1;
+  if (tiles <= kAlone * most_w) {
+    p.waves = tiles > 2 * 4 ? (uint32_t)(tiles / 2 + 3) / 4 * 4 : 4;
+    if (p.waves > most_w) p.waves = most_w;
+  } else {
+    p.waves = 4;
+    splits = 64 * most_w / blocks;
+    const uint64_t top = (tiles + kChunk - 1) / kChunk;
+    if (splits > top) splits = top;
+    if (splits > kMostSplits) splits = kMostSplits;
+    if (splits < 1) splits = 1;
+  }
   p.chunk = (uint32_t)((tiles + splits - 1) / splits);
   p.splits = (uint32_t)((tiles + p.chunk - 1) / p.chunk);
   return p;
@@ -780,19 +796,17 @@ uint64_t part_bytes(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_atten
 }
 
 template <int NB, int NQ, bool F16>
-void launch_attend(hipStream_t stream, const AttendArgs& a) {
+void launch_attend(hipStream_t stream, const AttendArgs& a, uint32_t waves) {
   const uint32_t z = a.t.batch + (a.t.starts ? 1 : 0);
-  hipLaunchKernelGGL((k_kv4_attend<NB, NQ, F16>), dim3(a.splits, a.q_tiles * a.c.heads, z), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((k_kv4_attend<NB, NQ, F16>), dim3(a.splits, a.q_tiles * a.c.heads, z), dim3(64 * waves), 0, stream, a);
 }
 
 template <int NB, bool F16>
-ecw_status launch_all(hipStream_t stream, const AttendArgs& a, uint32_t nq) {
-  if (nq == 1)
-    launch_attend<NB, 1, F16>(stream, a);
-  else if (nq == 2 || NB == 8)
-    launch_attend<NB, 2, F16>(stream, a);
+ecw_status launch_all(hipStream_t stream, const AttendArgs& a, const Plan& p) {
+  if (p.nq == 1)
+    launch_attend<NB, 1, F16>(stream, a, p.waves);
   else
-    launch_attend<NB, NB == 8 ? 2 : 4, F16>(stream, a);
+    launch_attend<NB, 2, F16>(stream, a, p.waves);
   if (ecw_status s = launched("kv4_attend")) return s;
   if (a.splits == 1) return ECW_OK;
   const uint64_t all = (uint64_t)a.t.rows * a.q_heads, grid = (all + 3) / 4;
@@ -802,11 +816,11 @@ ecw_status launch_all(hipStream_t stream, const AttendArgs& a, uint32_t nq) {
 }
 
 template <bool F16>
-ecw_status launch_dim(hipStream_t stream, const AttendArgs& a, uint32_t nq) {
+ecw_status launch_dim(hipStream_t stream, const AttendArgs& a, const Plan& p) {
   switch (a.c.dim) {
-    case 64: return launch_all<2, F16>(stream, a, nq);
-    case 128: return launch_all<4, F16>(stream, a, nq);
-    default: return launch_all<8, F16>(stream, a, nq);
+    case 64: return launch_all<2, F16>(stream, a, p);
+    case 128: return launch_all<4, F16>(stream, a, p);
+    default: return launch_all<8, F16>(stream, a, p);
   }
 }
 
@@ -899,8 +913,8 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
   a.sinks = (int32_t)at->sinks;
   a.scale = at->scale * 1.44269504088896f;
   a.vec = aligned(q, 16) && q_row % 8 == 0 && q_head % 8 == 0;
-  return dtype == ECW_DT_F16 ? launch_dim<true>((hipStream_t)stream, a, p.nq)
-                             : launch_dim<false>((hipStream_t)stream, a, p.nq);
+  return dtype == ECW_DT_F16 ? launch_dim<true>((hipStream_t)stream, a, p)
+                             : launch_dim<false>((hipStream_t)stream, a, p);
 }
 
 }  // extern "C"
