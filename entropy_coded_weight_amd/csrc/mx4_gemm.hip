@@ -12,6 +12,7 @@
 // x needs no rounding.  In fp16 they are exact relative to the span's largest scale
 // when its scales span at most 2^23 (0.5 * 2^-23 is fp16's smallest number); the
 // span's sum is multiplied by that scale in fp32.  A wider span takes further passes.
+#include <atomic>
 #include <type_traits>
 
 #include "mx4_common.h"
@@ -128,46 +129,145 @@ __device__ __forceinline__ f32x4 span_product_mx4(f32x4 acc, u32x4 w, uint32_t s
                                                           (int)(sw >> 8 * g));
 }
 
-// A block computes 16 rows of w times 16 NT rows of x; its waves take the spans in
-// turn and join their sums through LDS, in the order of the waves.
-template <int ACT, int NT>
-__global__ void __launch_bounds__(1024) k_mx4_gemm_few(GemmArgs a, int y_dtype) {
-  extern __shared__ f32x4 part[];  // [waves][NT][64]
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+// Copies 16 (or 4) bytes per lane from global memory to LDS, lane after lane from `to`
+// on, without registers between.  The caller counts them: they are done when
+// `s_waitcnt vmcnt` says so.
+template <int BYTES>
+__device__ __forceinline__ void to_lds(const void* from, uint32_t to) {
+  static_assert(BYTES == 16 || BYTES == 4, "");
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+__device__ const u32x4 zeros16 = {0, 0, 0, 0};
+
+// ------------------------------------------------------------------ a few rows
+// A block computes 16 rows of w times 16 NT rows of x; its waves take pairs of spans in
+// turn and join their sums through LDS, in the order of the waves.  A wave copies w for up
+// to four turns straight to LDS, 8 rows of 128 bytes at a time, so that neighbouring lanes
+// read whole lines: as operands they would be 16-byte pieces of 16 rows.  16 bytes at
+// piece p of row r's 8 lie at p ^ stirred(r), so that the 16 lanes that LDS serves together
+// meet no bank twice.  Bound by reading w.
+__device__ __forceinline__ uint32_t stirred(uint32_t r) { return ((r >> 1) + 2) & 7; }
+
+constexpr uint32_t kTurns = 4;             // pairs of spans that a wave has in LDS
+constexpr uint32_t kTurnBytes = 16 * 128;  // 16 rows of w
+constexpr uint32_t few_waves(int nt) { return nt == 4 ? 8 : 16; }  // what a CU's registers hold
+
+// VEC: rows of 16-bit x are 16-byte aligned and a multiple of 8 columns.
+template <int ACT, int NT, bool VEC>
+__global__ void __launch_bounds__(64 * few_waves(NT)) k_mx4_gemm_few(GemmArgs a, int y_dtype) {
+  extern __shared__ __align__(16) uint8_t lds[];  // each wave's turns, then (over them) the sums
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const uint32_t lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r16 = lane & 15, g = lane >> 4;
   const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * NT);
-  const uint32_t n = min(n0 + r16, a.rows - 1);
-  const uint32_t spans = a.blocks / 4;
-  const uint8_t* w = a.w + (uint64_t)n * a.blocks * 16 + g * 16;
-  const uint8_t* ws = a.ws + (uint64_t)n * a.scales;
+  const uint32_t spans = a.blocks / 4, pairs = (spans + 1) / 2;
+
+  const uint8_t* from[2];  // the lane's 16 bytes of rows 0-7 and 8-15, in pair 0
+  bool late[2];            // whether they are of the pair's second span
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t row = i * 8 + (lane >> 3), piece = (lane & 7) ^ stirred(row);
+    from[i] = a.w + (uint64_t)min(n0 + row, a.rows - 1) * a.blocks * 16 + piece * 16;
+    late[i] = piece >= 4;
+  }
+  const uint8_t* ws = a.ws + (uint64_t)min(n0 + r16, a.rows - 1) * a.scales;
+  const uint8_t* xrow[NT];
+  const uint8_t* xs[NT];
   f32x4 acc[NT];
-  uint64_t m[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    m[t] = min(m0 + t * 16 + r16, a.batch - 1);
+    const uint64_t m = min(m0 + t * 16 + r16, a.batch - 1);
+    xrow[t] = static_cast<const uint8_t*>(a.x) + (ACT == kActMX4 ? m * a.blocks * 16 : (int64_t)m * a.x_stride * 2);
+    if constexpr (ACT == kActMX4) xs[t] = a.xs + m * a.scales;
   }
-  for (uint32_t s = wave; s < spans; s += waves) {
-    const u32x4 wv = *reinterpret_cast<const u32x4*>(w + (uint64_t)s * 64);
-    const uint32_t sw = *reinterpret_cast<const uint32_t*>(ws + s * 4);
-    if constexpr (ACT == kActMX4) {
+  constexpr int kWords = ACT == kActMX4 ? 1 : 4;
+  // the operands of x in span s (in the last span past the end)
+  auto load_x = [&](u32x4 (&x)[NT][kWords], uint32_t (&sx)[NT], uint32_t s) {
+    s = min(s, spans - 1);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint8_t* x = static_cast<const uint8_t*>(a.x) + m[t] * a.blocks * 16 + (uint64_t)s * 64 + g * 16;
-        const uint32_t sx = *reinterpret_cast<const uint32_t*>(a.xs + m[t] * a.scales + s * 4);
-        acc[t] = span_product_mx4(acc[t], wv, sw, g, *reinterpret_cast<const u32x4*>(x), sx);
+    for (int t = 0; t < NT; ++t) {
+      if constexpr (ACT == kActMX4) {
+        x[t][0] = *reinterpret_cast<const u32x4*>(xrow[t] + (uint64_t)s * 64 + g * 16);
+        sx[t] = *reinterpret_cast<const uint32_t*>(xs[t] + s * 4);
+      } else {
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(xrow[t]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t c = s * 128 + g * 32 + j * 8;
+          if constexpr (VEC) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(row + min(c, a.cols - 8));
+            x[t][j] = c < a.cols ? v : u32x4{0, 0, 0, 0};
+          } else {
+            x[t][j] = load_oct16(row, c, a.cols, false).v;
+          }
+        }
       }
-    } else {
-      u32x4 x[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[t][j] = load_oct16(static_cast<const uint16_t*>(a.x) + m[t] * a.x_stride, s * 128 + g * 32 + j * 8,
-                               a.cols, a.vec).v;
-      span_product<ACT, NT>(acc, wv, sw, g, x);
     }
+  };
+
+  for (uint32_t first = wave; first < pairs; first += waves * kTurns) {
+#pragma unroll
+    for (uint32_t k = 0; k < kTurns; ++k) {
+      const uint32_t p = first + k * waves;
+      if (p < pairs) {
+        // an odd last span has no second half to copy: those lanes copy the first again
+        const uint32_t half = p * 2 + 1 < spans ? 0 : 64;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          to_lds<16>(from[i] + (uint64_t)p * 128 - (late[i] ? half : 0),
+                     base + (wave * kTurns + k) * kTurnBytes + i * 1024);
+      }
+    }
+    u32x2 sw[kTurns];
+#pragma unroll
+    for (uint32_t k = 0; k < kTurns; ++k)
+      sw[k] = *reinterpret_cast<const u32x2*>(ws + min(first + k * waves, pairs - 1) * 8);
+    u32x4 x[NT][kWords];
+    uint32_t sx[NT];
+    load_x(x, sx, first * 2);
+    wait_copies<0>();
+#pragma unroll
+    for (uint32_t i = 0; i < 2 * kTurns; ++i) {
+      const uint32_t k = i / 2, h = i % 2, s = (first + k * waves) * 2 + h;
+      // one row tile of x: the next span's is on its way while this one is multiplied
+      u32x4 next[NT][kWords];
+      uint32_t snext[NT];
+      const uint32_t after = h == 0 ? s + 1 : (first + (k + 1) * waves) * 2;
+      if (NT == 1 && i + 1 < 2 * kTurns) load_x(next, snext, after);
+      const u32x4 wv = *reinterpret_cast<const u32x4*>(lds + (wave * kTurns + k) * kTurnBytes + r16 * 128 +
+                                                       ((h * 4 + g) ^ stirred(r16)) * 16);
+      if (s < spans) {
+        if constexpr (ACT == kActMX4) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[t] = span_product_mx4(acc[t], wv, sw[k][h], g, x[t][0], sx[t]);
+        } else {
+          span_product<ACT, NT>(acc, wv, sw[k][h], g, x);
+        }
+      }
+      if (i + 1 < 2 * kTurns) {
+        if (NT > 1) load_x(next, snext, after);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          sx[t] = snext[t];
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) x[t][j] = next[t][j];
+        }
+      }
+    }
+    wait_copies<0>();  // this wave's reads of LDS are done before it copies again
   }
+  __syncthreads();
+  f32x4* part = reinterpret_cast<f32x4*>(lds);  // [waves][NT][64]
 #pragma unroll
   for (int t = 0; t < NT; ++t) part[(wave * NT + t) * 64 + lane] = acc[t];
   __syncthreads();
@@ -178,10 +278,12 @@ __global__ void __launch_bounds__(1024) k_mx4_gemm_few(GemmArgs a, int y_dtype) 
     const uint32_t row = n0 + (i & 15), b = m0 + i / 64 * 16 + (i >> 4 & 3) * 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (row < a.rows && b + r < a.batch) with_type(y_dtype, [&](auto dt) { store_y<dt.value>(a.y, (uint64_t)(b + r) * a.rows + row, sum[r]); });
+      if (row < a.rows && b + r < a.batch)
+        with_type(y_dtype, [&](auto dt) { store_y<dt.value>(a.y, (uint64_t)(b + r) * a.rows + row, sum[r]); });
   }
 }
 
+// ------------------------------------------------------------------ many rows
 // A block's place among the tiles: blocks go to the 8 dies in turn, so each die takes a
 // contiguous run of tiles, and within it 8 tiles of x rows stand next to each other, for
 // the die's L2 to hold what its blocks share.
@@ -287,25 +389,6 @@ __global__ void __launch_bounds__(256, 2) k_mx4_gemm_loose(GemmArgs a, uint32_t 
         }
   });
 }
-
-// ------------------------------------------------------------------ many rows
-// Copies 16 (or 4) bytes per lane from global memory to LDS, lane after lane from `to`
-// on, without registers between.  The caller counts them: they are done when
-// `s_waitcnt vmcnt` says so.
-template <int BYTES>
-__device__ __forceinline__ void to_lds(const void* from, uint32_t to) {
-  static_assert(BYTES == 16 || BYTES == 4, "");
-  if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
-
-__device__ const u32x4 zeros16 = {0, 0, 0, 0};
 
 // 16 rows of 4 bits of a span are 1 KiB in LDS: row r's block b at place 4 r + (b ^
 // shifted(r)), so that four neighbouring lanes copy 64 neighbouring bytes and the 16
@@ -521,15 +604,33 @@ ecw_status check_weight(const void* codes, const void* scales, uint32_t rows, ui
   return ECW_OK;
 }
 
-template <int ACT, int NT>
-ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
+template <int ACT, int NT, bool VEC>
+ecw_status launch_few_as(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   const uint32_t nt = (a.rows + 15) / 16, mt = (a.batch + 16 * NT - 1) / (16 * NT), spans = a.blocks / 4;
   if (mt > 65535) return refuse(ECW_E_UNSUPPORTED, "batch too large for one launch");
+  const uint32_t pairs = (spans + 1) / 2;
+  // up to four pairs a wave, and waves enough to fill the card
   uint32_t waves = 4;
-  while (waves < 16 && (uint64_t)nt * mt * waves < 2048 && waves < spans) waves *= 2;
-  hipLaunchKernelGGL((k_mx4_gemm_few<ACT, NT>), dim3(nt, mt), dim3(waves * 64), waves * NT * 64 * sizeof(f32x4),
-                     stream, a, y_dtype);
+  while (waves < few_waves(NT) && (pairs > waves * kTurns || ((uint64_t)nt * mt * waves < 2048 && waves < pairs))) waves *= 2;
+  const uint32_t lds = waves * (kTurns * kTurnBytes > NT * 1024 ? kTurns * kTurnBytes : NT * 1024);
+  auto* fn = k_mx4_gemm_few<ACT, NT, VEC>;
+  static std::atomic<bool> allowed{false};  // more than 64 KiB of LDS, once
+  if (lds > 64 * 1024 && !allowed.load(std::memory_order_relaxed)) {
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            160 * 1024) != hipSuccess) {
+      (void)hipGetLastError();
+      return refuse(ECW_E_HIP, "hipFuncSetAttribute failed");
+    }
+    allowed.store(true, std::memory_order_relaxed);
+  }
+  hipLaunchKernelGGL(fn, dim3(nt, mt), dim3(waves * 64), lds, stream, a, y_dtype);
   return launched("mx4_gemm");
+}
+
+template <int ACT, int NT>
+ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
+  if (ACT == kActMX4 || (a.vec && a.cols % 8 == 0)) return launch_few_as<ACT, NT, true>(stream, a, y_dtype);
+  return launch_few_as<ACT, NT, ACT == kActMX4>(stream, a, y_dtype);
 }
 
 template <int ACT, int WM, int WN, int TM, int TN, int NS>
