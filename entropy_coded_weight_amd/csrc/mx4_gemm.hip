@@ -148,27 +148,29 @@ __device__ __forceinline__ void wait_copies() {
 __device__ const u32x4 zeros16 = {0, 0, 0, 0};
 
 // ------------------------------------------------------------------ a few rows
-// A block computes 16 rows of w times 16 NT rows of x; its waves take pairs of spans in
+// A block computes 16 rows of w times up to 16 rows of x; its waves take pairs of spans in
 // turn and join their sums through LDS, in the order of the waves.  A wave copies w for up
 // to four turns straight to LDS, 8 rows of 128 bytes at a time, so that neighbouring lanes
 // read whole lines: as operands they would be 16-byte pieces of 16 rows.  16 bytes at
 // piece p of row r's 8 lie at p ^ stirred(r), so that the 16 lanes that LDS serves together
-// meet no bank twice.  Bound by reading w.
+// meet no bank twice.  The first turn's x is asked for before w, later turns' one turn
+// ahead: behind w in a CU's queue, x took 3 of 11.8 us for one row by 14336 x 4096 (10.7
+// us; 31 MB of w).  Bound by reading w.
 __device__ __forceinline__ uint32_t stirred(uint32_t r) { return ((r >> 1) + 2) & 7; }
 
 constexpr uint32_t kTurns = 4;             // pairs of spans that a wave has in LDS
 constexpr uint32_t kTurnBytes = 16 * 128;  // 16 rows of w
-constexpr uint32_t few_waves(int nt) { return nt == 4 ? 8 : 16; }  // what a CU's registers hold
+constexpr uint32_t kFewWaves = 16;         // at most
 
-// VEC: rows of 16-bit x are 16-byte aligned and a multiple of 8 columns.
-template <int ACT, int NT, bool VEC>
-__global__ void __launch_bounds__(64 * few_waves(NT)) k_mx4_gemm_few(GemmArgs a, int y_dtype) {
+// VEC: rows of 16-bit x are 16-byte aligned, a multiple of 8 columns, and end within 2^31 bytes.
+template <int ACT, bool VEC>
+__global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int y_dtype) {
   extern __shared__ __align__(16) uint8_t lds[];  // each wave's turns, then (over them) the sums
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r16 = lane & 15, g = lane >> 4;
-  const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * NT);
+  const uint32_t n0 = blockIdx.x * 16;
   const uint32_t spans = a.blocks / 4, pairs = (spans + 1) / 2;
 
   const uint8_t* from[2];  // the lane's 16 bytes of rows 0-7 and 8-15, in pair 0
@@ -180,42 +182,50 @@ __global__ void __launch_bounds__(64 * few_waves(NT)) k_mx4_gemm_few(GemmArgs a,
     late[i] = piece >= 4;
   }
   const uint8_t* ws = a.ws + (uint64_t)min(n0 + r16, a.rows - 1) * a.scales;
-  const uint8_t* xrow[NT];
-  const uint8_t* xs[NT];
-  f32x4 acc[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint64_t m = min(m0 + t * 16 + r16, a.batch - 1);
-    xrow[t] = static_cast<const uint8_t*>(a.x) + (ACT == kActMX4 ? m * a.blocks * 16 : (int64_t)m * a.x_stride * 2);
-    if constexpr (ACT == kActMX4) xs[t] = a.xs + m * a.scales;
-  }
+  const uint64_t m = min(r16, a.batch - 1);
+  const uint8_t* xrow = static_cast<const uint8_t*>(a.x) + (ACT == kActMX4 ? m * a.blocks * 16 : (int64_t)m * a.x_stride * 2);
+  const uint8_t* xs = ACT == kActMX4 ? a.xs + m * a.scales : nullptr;
   constexpr int kWords = ACT == kActMX4 ? 1 : 4;
+  // 16-bit x as a buffer of bytes: what is past its end, columns or rows, reads as zero
+  // and fetches nothing
+  const auto xbuf = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(a.x), 0,
+                                                      (uint32_t)(((a.batch - 1) * a.x_stride + a.cols) * 2), 0x00027000);
+  const uint32_t xoff = r16 < a.batch ? (uint32_t)(r16 * a.x_stride * 2) : 1u << 31;
+  struct Span {
+    u32x4 x[1][kWords];
+    uint32_t sx;
+  };
   // the operands of x in span s (in the last span past the end)
-  auto load_x = [&](u32x4 (&x)[NT][kWords], uint32_t (&sx)[NT], uint32_t s) {
+  auto load_x = [&](Span& to, uint32_t s) {
     s = min(s, spans - 1);
+    if constexpr (ACT == kActMX4) {
+      to.x[0][0] = *reinterpret_cast<const u32x4*>(xrow + (uint64_t)s * 64 + g * 16);
+      to.sx = *reinterpret_cast<const uint32_t*>(xs + s * 4);
+    } else {
+      const uint16_t* row = reinterpret_cast<const uint16_t*>(xrow);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if constexpr (ACT == kActMX4) {
-        x[t][0] = *reinterpret_cast<const u32x4*>(xrow[t] + (uint64_t)s * 64 + g * 16);
-        sx[t] = *reinterpret_cast<const uint32_t*>(xs[t] + s * 4);
-      } else {
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(xrow[t]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t c = s * 128 + g * 32 + j * 8;
-          if constexpr (VEC) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(row + min(c, a.cols - 8));
-            x[t][j] = c < a.cols ? v : u32x4{0, 0, 0, 0};
-          } else {
-            x[t][j] = load_oct16(row, c, a.cols, false).v;
-          }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t c = s * 128 + g * 32 + j * 8;
+        if constexpr (VEC) {
+          to.x[0][j] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, c < a.cols ? xoff + c * 2 : ~0u, 0, 0));
+        } else {
+          to.x[0][j] = load_oct16(row, c, a.cols, false).v;
         }
       }
     }
   };
 
+  f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
   for (uint32_t first = wave; first < pairs; first += waves * kTurns) {
+    u32x2 sw[kTurns];
+#pragma unroll
+    for (uint32_t k = 0; k < kTurns; ++k)
+      sw[k] = *reinterpret_cast<const u32x2*>(ws + min(first + k * waves, pairs - 1) * 8);
+    Span x[2];
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h) load_x(x[h], first * 2 + h);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (uint32_t k = 0; k < kTurns; ++k) {
       const uint32_t p = first + k * waves;
@@ -228,58 +238,40 @@ __global__ void __launch_bounds__(64 * few_waves(NT)) k_mx4_gemm_few(GemmArgs a,
                      base + (wave * kTurns + k) * kTurnBytes + i * 1024);
       }
     }
-    u32x2 sw[kTurns];
-#pragma unroll
-    for (uint32_t k = 0; k < kTurns; ++k)
-      sw[k] = *reinterpret_cast<const u32x2*>(ws + min(first + k * waves, pairs - 1) * 8);
-    u32x4 x[NT][kWords];
-    uint32_t sx[NT];
-    load_x(x, sx, first * 2);
     wait_copies<0>();
 #pragma unroll
-    for (uint32_t i = 0; i < 2 * kTurns; ++i) {
-      const uint32_t k = i / 2, h = i % 2, s = (first + k * waves) * 2 + h;
-      // one row tile of x: the next span's is on its way while this one is multiplied
-      u32x4 next[NT][kWords];
-      uint32_t snext[NT];
-      const uint32_t after = h == 0 ? s + 1 : (first + (k + 1) * waves) * 2;
-      if (NT == 1 && i + 1 < 2 * kTurns) load_x(next, snext, after);
-      const u32x4 wv = *reinterpret_cast<const u32x4*>(lds + (wave * kTurns + k) * kTurnBytes + r16 * 128 +
-                                                       ((h * 4 + g) ^ stirred(r16)) * 16);
-      if (s < spans) {
-        if constexpr (ACT == kActMX4) {
+    for (uint32_t k = 0; k < kTurns; ++k) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[t] = span_product_mx4(acc[t], wv, sw[k][h], g, x[t][0], sx[t]);
-        } else {
-          span_product<ACT, NT>(acc, wv, sw[k][h], g, x);
+      for (uint32_t h = 0; h < 2; ++h) {
+        const uint32_t s = (first + k * waves) * 2 + h;
+        Span& now = x[h];
+        const u32x4 wv = *reinterpret_cast<const u32x4*>(lds + (wave * kTurns + k) * kTurnBytes + r16 * 128 +
+                                                         ((h * 4 + g) ^ stirred(r16)) * 16);
+        if (s < spans) {
+          if constexpr (ACT == kActMX4)
+            acc[0] = span_product_mx4(acc[0], wv, sw[k][h], g, now.x[0][0], now.sx);
+          else
+            span_product<ACT, 1>(acc, wv, sw[k][h], g, now.x);
         }
-      }
-      if (i + 1 < 2 * kTurns) {
-        if (NT > 1) load_x(next, snext, after);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          sx[t] = snext[t];
-#pragma unroll
-          for (int j = 0; j < kWords; ++j) x[t][j] = next[t][j];
-        }
+        if (k + 1 < kTurns) load_x(now, (first + (k + 1) * waves) * 2 + h);
       }
     }
     wait_copies<0>();  // this wave's reads of LDS are done before it copies again
   }
   __syncthreads();
-  f32x4* part = reinterpret_cast<f32x4*>(lds);  // [waves][NT][64]
-#pragma unroll
-  for (int t = 0; t < NT; ++t) part[(wave * NT + t) * 64 + lane] = acc[t];
+  f32x4* part = reinterpret_cast<f32x4*>(lds);  // [waves][64]
+  part[wave * 64 + lane] = acc[0];
   __syncthreads();
-  // lane l of tile t: rows 4 (l / 16) .. + 3 of x, row l % 16 of w
-  for (uint32_t i = threadIdx.x; i < NT * 64; i += blockDim.x) {
-    f32x4 sum = part[i];
-    for (uint32_t v = 1; v < waves; ++v) sum += part[v * NT * 64 + i];
-    const uint32_t row = n0 + (i & 15), b = m0 + i / 64 * 16 + (i >> 4 & 3) * 4;
+  // lane l: rows 4 (l / 16) .. + 3 of x, row l % 16 of w
+  if (wave == 0) {
+    f32x4 sum = part[lane];
+    for (uint32_t v = 1; v < waves; ++v) sum += part[v * 64 + lane];
+    with_type(y_dtype, [&](auto dt) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (row < a.rows && b + r < a.batch)
-        with_type(y_dtype, [&](auto dt) { store_y<dt.value>(a.y, (uint64_t)(b + r) * a.rows + row, sum[r]); });
+      for (int r = 0; r < 4; ++r)
+        if (n0 + r16 < a.rows && g * 4 + r < a.batch)
+          store_y<dt.value>(a.y, (uint64_t)(g * 4 + r) * a.rows + n0 + r16, sum[r]);
+    });
   }
 }
 
@@ -396,18 +388,20 @@ __global__ void __launch_bounds__(256, 2) k_mx4_gemm_loose(GemmArgs a, uint32_t 
 __device__ __forceinline__ uint32_t shifted(uint32_t r) { return (0u - (r >> 2)) & 3; }
 
 // A block of WM x WN waves multiplies 16 TM WM rows of x and 16 TN WN rows of w, a span
-// at a time, from NS stages in LDS that copies fill NS - 1 spans ahead.  Scales come for
-// four spans at once, into two places of their own.
-template <int ACT, int WM, int WN, int TM, int TN, int NS>
+// at a time, from NS stages in LDS that copies fill ahead.  EARLY: a wave reads a span's
+// operands from LDS while it multiplies the span before.  Scales come for four spans at
+// once, into places of their own.
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY>
 struct Tiles {
   static constexpr bool kX4 = ACT == kActMX4;
   static constexpr int kWaves = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
   static constexpr uint32_t kX = kX4 ? BM * 64 : BM * 256, kW = BN * 64, kStage = kX + kW;
   static constexpr uint32_t kScaleRows = (kX4 ? BM : 0) + BN;  // those of x first
-  static constexpr uint32_t kBytes = kStage * NS + 2 * kScaleRows * 16;
+  static constexpr uint32_t kScalePlaces = (NS + 3) / 4 + 1;
+  static constexpr uint32_t kBytes = kStage * NS + kScalePlaces * kScaleRows * 16;
   static constexpr int kXLoads = kX / 1024 / kWaves, kWLoads = kW / 1024 / kWaves;  // copies per wave and span
   static constexpr int kSLoads = (kScaleRows / 64 + kWaves - 1) / kWaves;           // per four spans
-  static_assert(kX % (1024 * kWaves) == 0 && kW % (1024 * kWaves) == 0 && NS <= 5, "");
+  static_assert(kX % (1024 * kWaves) == 0 && kW % (1024 * kWaves) == 0, "");
   static_assert(kBytes <= 160 * 1024, "");
 };
 
@@ -428,17 +422,22 @@ __device__ __forceinline__ void store_run(void* y, uint64_t at, const float (&v)
       for (int i = 0; i < N; i += 4)
         *reinterpret_cast<f32x4*>(static_cast<float*>(y) + at + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
     } else {
+      uint32_t w[N / 2];
 #pragma unroll
-      for (int i = 0; i < N; i += 8) {
-        u32x4 w;
+      for (int i = 0; i < N / 2; ++i) {
+        if constexpr (DT == ECW_DT_F16)
+          w[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
+        else
+          w[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+      }
+      uint16_t* o = static_cast<uint16_t*>(y) + at;
+      if constexpr (N % 8 == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (DT == ECW_DT_F16)
-            w[j] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[i + 2 * j], (_Float16)v[i + 2 * j + 1]});
-          else
-            w[j] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[i + 2 * j], (__bf16)v[i + 2 * j + 1]});
-        }
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(y) + at + i) = w;
+        for (int i = 0; i < N / 2; i += 4)
+          *reinterpret_cast<u32x4*>(o + 2 * i) = u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+      } else {
+        static_assert(N == 4, "");
+        *reinterpret_cast<u32x2*>(o) = u32x2{w[0], w[1]};
       }
     }
     return;
@@ -448,10 +447,10 @@ __device__ __forceinline__ void store_run(void* y, uint64_t at, const float (&v)
     if ((uint32_t)i < left) store_y<DT>(y, at + i, v[i]);
 }
 
-template <int ACT, int WM, int WN, int TM, int TN, int NS>
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY>
 __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint32_t m_tiles, uint32_t n_tiles,
                                                                 int y_dtype) {
-  using T = Tiles<ACT, WM, WN, TM, TN, NS>;
+  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY>;
   __shared__ __align__(16) uint8_t lds[T::kBytes];
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -497,7 +496,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       for (int i = 0; i < T::kSLoads; ++i) {
         const uint32_t part = wave + i * T::kWaves;
         if (part < T::kScaleRows / 64)
-          to_lds<16>(sp[i] + s * 4, base + T::kStage * NS + (span / 4 % 2) * T::kScaleRows * 16 + part * 1024);
+          to_lds<16>(sp[i] + s * 4, base + T::kStage * NS + (span / 4 % T::kScalePlaces) * T::kScaleRows * 16 + part * 1024);
       }
     }
     const uint32_t to = base + stage * T::kStage;
@@ -521,44 +520,83 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
 #pragma unroll
     for (int m = 0; m < TM; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint32_t wm = wave / WN * TM, wn = wave % WN * TN;  // first 16-row tiles of the wave
+  const uint32_t in = r16 * 4 + (g ^ shifted(r16));         // the lane's place in 16 rows of 4 bits
 
-#pragma unroll
-  for (int i = 0; i < NS - 1; ++i) fill(i, i);
-  uint32_t stage = 0, next = NS - 1;
-  for (uint32_t s = 0; s < spans; ++s) {
-    wait_copies<(NS - 2) * (T::kXLoads + T::kWLoads)>();  // or fewer left, if scales are among them
-    __builtin_amdgcn_s_barrier();  // this span is there, and the one before it is done with
-    fill(s + NS - 1, next);
+  struct Operands {
+    u32x4 x[TM][T::kX4 ? 1 : 4], w[TN];
+    uint32_t xs[TM], ws[TN];
+  };
+  auto read = [&](Operands& f, uint32_t s, uint32_t stage) {
     const uint8_t* at = lds + stage * T::kStage;
     const u32x4* x = reinterpret_cast<const u32x4*>(at);
     const u32x4* w = reinterpret_cast<const u32x4*>(at + T::kX);
-    const uint32_t* xs = reinterpret_cast<const uint32_t*>(lds + T::kStage * NS + (s / 4 % 2) * T::kScaleRows * 16) + s % 4;
+    const uint32_t* xs = reinterpret_cast<const uint32_t*>(lds + T::kStage * NS + (s / 4 % T::kScalePlaces) * T::kScaleRows * 16) + s % 4;
     const uint32_t* ws = xs + (T::kX4 ? T::BM * 4 : 0);
-    const uint32_t in = r16 * 4 + (g ^ shifted(r16));  // the lane's place in 16 rows of 4 bits
-    if constexpr (T::kX4) {
-      u32x4 xf[TM];
-      uint32_t xb[TM];
 #pragma unroll
-      for (int m = 0; m < TM; ++m) xf[m] = x[(wm + m) * 64 + in], xb[m] = xs[((wm + m) * 16 + r16) * 4];
-#pragma unroll
-      for (int n = 0; n < TN; ++n) {
-        const u32x4 wf = w[(wn + n) * 64 + in];
-        const uint32_t wb = ws[(wn * 16 + spread<TN>(n, r16)) * 4];
-#pragma unroll
-        for (int m = 0; m < TM; ++m) acc[n][m] = span_product_mx4(acc[n][m], xf[m], xb[m], g, wf, wb);
-      }
-    } else {
-      u32x4 xf[TM][4];
-#pragma unroll
-      for (int m = 0; m < TM; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) xf[m][j] = x[((wm + m) * 16 + r16) * 16 + ((4 * j + g) ^ r16)];
-#pragma unroll
-      for (int n = 0; n < TN; ++n)
-        span_product<ACT, TM>(acc[n], w[(wn + n) * 64 + in], ws[((wn + n) * 16 + r16) * 4], g, xf);
+    for (int n = 0; n < TN; ++n) {
+      f.w[n] = w[(wn + n) * 64 + in];
+      f.ws[n] = ws[(T::kX4 ? wn * 16 + spread<TN>(n, r16) : (wn + n) * 16 + r16) * 4];
     }
-    stage = stage + 1 == NS ? 0 : stage + 1;
-    next = next + 1 == NS ? 0 : next + 1;
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      if constexpr (T::kX4) {
+        f.x[m][0] = x[(wm + m) * 64 + in];
+        f.xs[m] = xs[((wm + m) * 16 + r16) * 4];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.x[m][j] = x[((wm + m) * 16 + r16) * 16 + ((4 * j + g) ^ r16)];
+      }
+    }
+  };
+  auto multiply = [&](const Operands& f) {
+#pragma unroll
+    for (int n = 0; n < TN; ++n) {
+      if constexpr (T::kX4) {
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+          acc[n][m] = span_product_mx4(acc[n][m], f.x[m][0], f.xs[m], g, f.w[n], f.ws[n]);
+      } else {
+        span_product<ACT, TM>(acc[n], f.w[n], f.ws[n], g, f.x);
+      }
+    }
+  };
+  constexpr int kCopies = T::kXLoads + T::kWLoads;  // of a span; scales may be among those waited for too
+  uint32_t stage = 0;                               // of the span that is multiplied
+  if constexpr (EARLY) {
+    auto step = [&](uint32_t s, const Operands& now, Operands& next) {
+      wait_copies<(NS - 2) * kCopies>();
+      __builtin_amdgcn_s_barrier();  // the next span is there, and this one's stage is read
+      fill(s + NS, stage);
+      stage = stage + 1 == NS ? 0 : stage + 1;
+      read(next, s + 1, stage);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(now);
+    };
+#pragma unroll
+    for (int i = 0; i < NS; ++i) fill(i, i);
+    wait_copies<(NS - 1) * kCopies>();
+    __builtin_amdgcn_s_barrier();
+    Operands even, odd;
+    read(even, 0, 0);
+    for (uint32_t s = 0; s < spans; s += 2) {
+      step(s, even, odd);
+      if (s + 1 == spans) break;
+      step(s + 1, odd, even);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) fill(i, i);
+    uint32_t before = NS - 1;  // the stage of the span before
+    for (uint32_t s = 0; s < spans; ++s) {
+      wait_copies<(NS - 2) * kCopies>();
+      __builtin_amdgcn_s_barrier();  // this span is there, and the one before it is done with
+      fill(s + NS - 1, before);
+      Operands now;
+      read(now, s, stage);
+      multiply(now);
+      before = stage;
+      stage = stage + 1 == NS ? 0 : stage + 1;
+    }
   }
   wait_copies<0>();
   with_type(y_dtype, [&](auto dt) {
@@ -604,16 +642,14 @@ ecw_status check_weight(const void* codes, const void* scales, uint32_t rows, ui
   return ECW_OK;
 }
 
-template <int ACT, int NT, bool VEC>
-ecw_status launch_few_as(hipStream_t stream, const GemmArgs& a, int y_dtype) {
-  const uint32_t nt = (a.rows + 15) / 16, mt = (a.batch + 16 * NT - 1) / (16 * NT), spans = a.blocks / 4;
-  if (mt > 65535) return refuse(ECW_E_UNSUPPORTED, "batch too large for one launch");
-  const uint32_t pairs = (spans + 1) / 2;
+template <int ACT, bool VEC>
+ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
+  const uint32_t nt = (a.rows + 15) / 16, pairs = (a.blocks / 4 + 1) / 2;
   // up to four pairs a wave, and waves enough to fill the card
   uint32_t waves = 4;
-  while (waves < few_waves(NT) && (pairs > waves * kTurns || ((uint64_t)nt * mt * waves < 2048 && waves < pairs))) waves *= 2;
-  const uint32_t lds = waves * (kTurns * kTurnBytes > NT * 1024 ? kTurns * kTurnBytes : NT * 1024);
-  auto* fn = k_mx4_gemm_few<ACT, NT, VEC>;
+  while (waves < kFewWaves && (pairs > waves * kTurns || ((uint64_t)nt * waves < 2048 && waves < pairs))) waves *= 2;
+  const uint32_t lds = waves * kTurns * kTurnBytes;
+  auto* fn = k_mx4_gemm_few<ACT, VEC>;
   static std::atomic<bool> allowed{false};  // more than 64 KiB of LDS, once
   if (lds > 64 * 1024 && !allowed.load(std::memory_order_relaxed)) {
     if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -623,43 +659,61 @@ ecw_status launch_few_as(hipStream_t stream, const GemmArgs& a, int y_dtype) {
     }
     allowed.store(true, std::memory_order_relaxed);
   }
-  hipLaunchKernelGGL(fn, dim3(nt, mt), dim3(waves * 64), lds, stream, a, y_dtype);
+  hipLaunchKernelGGL(fn, dim3(nt), dim3(waves * 64), lds, stream, a, y_dtype);
   return launched("mx4_gemm");
 }
 
-template <int ACT, int NT>
-ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
-  if (ACT == kActMX4 || (a.vec && a.cols % 8 == 0)) return launch_few_as<ACT, NT, true>(stream, a, y_dtype);
-  return launch_few_as<ACT, NT, ACT == kActMX4>(stream, a, y_dtype);
+uint64_t tiles(const GemmArgs& a, uint32_t bm, uint32_t bn) {
+  return (uint64_t)((a.batch + bm - 1) / bm) * ((a.rows + bn - 1) / bn);
 }
 
-template <int ACT, int WM, int WN, int TM, int TN, int NS>
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY>
 ecw_status launch_tile(hipStream_t stream, const GemmArgs& a, int y_dtype) {
-  using T = Tiles<ACT, WM, WN, TM, TN, NS>;
+  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY>;
   const uint32_t m_tiles = (a.batch + T::BM - 1) / T::BM, n_tiles = (a.rows + T::BN - 1) / T::BN;
   if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
-  hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves), 0,
+  hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS, EARLY>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves), 0,
                      stream, a, m_tiles, n_tiles, y_dtype);
   return launched("mx4_gemm");
 }
 
+// Tiles by size: the smallest that leaves no CU two of them, for spans are waited for and
+// small ones wait least; when there are more, the largest, which reads least.  Measured
+// with bf16 x, in us (64x64, 64x128, 128x128, 128x256): 64 rows by 4096 x 14336 60.5, 67.7,
+// 104, 161; 1024 by 4096 x 4096 -, 49.9, 38.7, 54.4; 512 by 14336 x 4096 -, 93, 75, 63.
 template <int ACT>
 ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
-  if (a.batch <= 16) return launch_few<ACT, 1>(stream, a, y_dtype);
-  if (a.batch <= 32) return launch_few<ACT, 2>(stream, a, y_dtype);
-  if (a.batch > 64) {
-    if constexpr (ACT == kActMX4) {
-      return launch_tile<ACT, 2, 4, 8, 4, 3>(stream, a, y_dtype);
-    } else {
-      if (a.vec && a.cols % 8 == 0) return launch_tile<ACT, 2, 4, 4, 2, 3>(stream, a, y_dtype);
-      const uint32_t m_tiles = (a.batch + 127) / 128, n_tiles = (a.rows + 127) / 128;
-      if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
-      hipLaunchKernelGGL(k_mx4_gemm_loose<ACT>, dim3(m_tiles * n_tiles), dim3(256), 0, stream, a, m_tiles, n_tiles,
-                         y_dtype);
-      return launched("mx4_gemm");
+  constexpr uint64_t kCus = 256;
+  // A few rows go a block per 16 rows of w, which reads x once for each: more rows and a
+  // short K are better off in tiles (16 rows by 14336 x 4096 22.6 and 13.8 us, 4 rows 14.5;
+  // by 4096 x 14336 21.8 and 37.8).
+  const bool few = a.batch <= 4 || (a.batch <= 16 && (tiles(a, 32, 64) < kCus / 2 || a.blocks > 4 * 48));
+  if constexpr (ACT == kActMX4) {
+    if (few) return launch_few<ACT, true>(stream, a, y_dtype);
+    if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 5, true>(stream, a, y_dtype);
+    if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 6, true>(stream, a, y_dtype);
+    if (tiles(a, 128, 256) <= kCus) return launch_tile<ACT, 2, 4, 4, 4, 4, true>(stream, a, y_dtype);
+    return launch_tile<ACT, 2, 4, 8, 4, 3, false>(stream, a, y_dtype);
+  } else {
+    const bool vec = a.vec && a.cols % 8 == 0;
+    if (vec) {
+      if (few) {
+        const bool near = ((uint64_t)(a.batch - 1) * (uint64_t)a.x_stride + a.cols) >> 30 == 0;
+        return near ? launch_few<ACT, true>(stream, a, y_dtype) : launch_few<ACT, false>(stream, a, y_dtype);
+      }
+      if (a.batch <= 32) return launch_tile<ACT, 1, 4, 2, 1, 5, true>(stream, a, y_dtype);
+      if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 4, true>(stream, a, y_dtype);
+      if (tiles(a, 64, 128) <= kCus) return launch_tile<ACT, 2, 4, 2, 2, 5, true>(stream, a, y_dtype);
+      if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 3, false>(stream, a, y_dtype);
+      return launch_tile<ACT, 2, 4, 4, 4, 3, false>(stream, a, y_dtype);
     }
+    if (a.batch <= 16) return launch_few<ACT, false>(stream, a, y_dtype);
+    const uint32_t m_tiles = (a.batch + 127) / 128, n_tiles = (a.rows + 127) / 128;
+    if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
+    hipLaunchKernelGGL(k_mx4_gemm_loose<ACT>, dim3(m_tiles * n_tiles), dim3(256), 0, stream, a, m_tiles, n_tiles,
+                       y_dtype);
+    return launched("mx4_gemm");
   }
-  return launch_few<ACT, 4>(stream, a, y_dtype);
 }
 
 ecw_status check_output(const void* y, int y_dtype, uint32_t batch) {

@@ -285,3 +285,29 @@ def test_refusals():
         ecw.mx4_quantize(x, out=w)
     with pytest.raises(ValueError):
         ecw.MX4Tensor(w.codes, w.scales, 16, 200)
+
+
+@pytest.mark.parametrize("acts", ["bf16", "fp16", "mx4"])
+@pytest.mark.parametrize("batch,rows,cols", [(5, 4100, 160), (12, 8200, 96), (40, 4112, 200), (70, 16400, 128),
+                                             (200, 8200, 264), (260, 16500, 136), (600, 12400, 72), (1100, 8300, 40)])
+def test_gemm_every_tile_size(batch, rows, cols, acts):
+    """Sizes on both sides of each rule that picks a tile."""
+    _say("gemm tiles", batch, rows, cols, acts)
+    w = _matrix(rows, cols, torch.bfloat16, seed=1, spread=1.0)
+    x = _matrix(batch, cols, torch.float16 if acts == "fp16" else torch.bfloat16, seed=3, spread=0)
+    t = ecw.mx4_quantize(w)
+    if acts == "mx4":
+        _check_product(w, x, t.gemm(ecw.mx4_quantize(x)), R.rounded(F64(x)))
+    else:
+        _check_product(w, x, t.gemm(x))
+
+
+def test_gemm_rows_far_apart():
+    """Rows of x more than 2^31 bytes from the first."""
+    _say("gemm far rows")
+    flat = torch.zeros((1 << 30) * 2 + 512, dtype=torch.bfloat16, device="cuda")
+    for batch in (3, 40):
+        x = flat.as_strided((batch, 96), ((1 << 31) // batch // 8 * 8, 1))
+        x.copy_(_matrix(batch, 96, torch.bfloat16, seed=3, spread=0))
+        w = _matrix(50, 96, torch.bfloat16, seed=1, spread=0)
+        _check_product(w, x, ecw.mx4_quantize(w).gemm(x))
