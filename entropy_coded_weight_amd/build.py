@@ -19,6 +19,22 @@ HIP_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-mcode-object-version=5", "-mllvm", "-amdgpu-kernarg-preload-count=11", "-Wall", "-Wno-unused-result",
              f"-I{ROOT}"]
+# the torch binding of the 4-bit calls: host code against torch's headers
+BIND = os.path.join(HERE, "_mx4.so")
+
+
+def _bind_flags():
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return (["-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             "-D__HIP_PLATFORM_AMD__=1", f"-I{sysconfig.get_paths()['include']}", f"-I{os.environ.get('ROCM_PATH', '/opt/rocm')}/include"]
+            + [f"-isystem{p}" for p in include_paths()],
+            [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"])
+
+
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{ROOT}"]
 
 
@@ -46,6 +62,9 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs, "-lpthread"], verbose)
     os.replace(tmp, LIB)
+    flags, libs = _bind_flags()
+    _run(["g++", *flags, os.path.join(CSRC, "mx4_bind.cpp"), "-o", BIND + ".tmp", *libs], verbose)
+    os.replace(BIND + ".tmp", BIND)
     return LIB
 
 

@@ -171,7 +171,7 @@ struct AttendArgs {
   int64_t q_row, q_head;  // strides
   uint32_t group, q_heads, q_tiles, splits;
   uint32_t chunk;         // tiles of one split
-  uint32_t per_page;      // 2^32 / tiles of a page, rounded up
+  uint32_t per_page;      // 2^32 / tiles of a page, rounded up; 0 for one
   int32_t window, sinks;  // window 0: none
   float scale;            // times log2 e
   bool vec;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendAr
     // is known by then.  A tile without a page, or none at all, loads page 0 and is passed
     // over: loads on a condition would have the wave wait for all of them each time.
     auto start_of = [&](int32_t i) { return (i < sink_tiles ? i : i - sink_tiles + first_tile) * 32; };
-    auto page_index = [&](int32_t t0) { return __umulhi((uint32_t)t0 / 32, a.per_page); };
+    auto page_index = [&](int32_t t0) { return a.per_page ? __umulhi((uint32_t)t0 / 32, a.per_page) : (uint32_t)t0 / 32; };
     auto page_of = [&](int32_t i) { return i < to ? table[page_index(start_of(i))] : -1; };
     auto fetch = [&](Tile<NB>& t, int32_t i, int32_t page) {
       const bool ok = (uint32_t)page < a.c.pages;
@@ -908,7 +908,7 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
   a.splits = p.splits;
   a.chunk = p.chunk;
   const uint32_t page_tiles = cache->page_tokens / 32;
-  a.per_page = (uint32_t)(((uint64_t(1) << 32) + page_tiles - 1) / page_tiles);
+  a.per_page = page_tiles == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + page_tiles - 1) / page_tiles);
   a.window = (int32_t)at->window;
   a.sinks = (int32_t)at->sinks;
   a.scale = at->scale * 1.44269504088896f;

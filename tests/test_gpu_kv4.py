@@ -179,6 +179,16 @@ def test_long_sequences_are_split_and_joined(dim, n):
     bed.check(bed.cache.attend(q, bed.table, I32(bed.lens), window=1000, sinks=9), q, [n, n], 1000, 9)
 
 
+@pytest.mark.parametrize("page", [32, 96, 128, 416, 4096])
+@pytest.mark.parametrize("n", [1, 20])
+def test_page_sizes(page, n):
+    _say("attend pages", page, n)
+    bed = Bed([37, 900, 1300], 1, 64, page=page)
+    q = _normal(83, 3 * n, 3, 64)
+    for window, sinks in ((0, 0), (300, 5)):
+        bed.check(bed.cache.attend(q, bed.table, I32(bed.lens), window=window, sinks=sinks), q, [n] * 3, window, sinks)
+
+
 @pytest.mark.parametrize("n", [1, 6, 40])
 def test_missing_pages_and_rows_that_see_nothing(n):
     _say("attend missing", n)

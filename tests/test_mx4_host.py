@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import entropy_coded_weight_amd as ecw
-from entropy_coded_weight_amd import mx4
+from tests import mx4_abi as mx4
 
 OK, INVALID, UNSUPPORTED = 0, 1, 2
 P = 1 << 20  # an aligned address that nothing reads
