@@ -171,6 +171,8 @@ struct AttendArgs {
   int64_t q_row, q_head;  // strides
   uint32_t group, q_heads, q_tiles, splits;
   uint32_t chunk;         // tiles of one split
+  uint32_t rows_each;     // rows / batch
+  uint32_t per_group;     // 2^32 / group, rounded up
   uint32_t per_page;      // 2^32 / tiles of a page, rounded up; 0 for one
   int32_t window, sinks;  // window 0: none
   float scale;            // times log2 e
@@ -454,7 +456,7 @@ __device__ void none(const AttendArgs& a) {
   const uint32_t hi = min((uint32_t)max(a.t.starts[a.t.batch], (int32_t)lo), a.t.rows);
   const uint64_t all = (uint64_t)a.t.rows * a.q_heads, before = (uint64_t)lo * a.q_heads;
   const uint64_t nobody = before + (uint64_t)(a.t.rows - hi) * a.q_heads;
-  for (uint64_t e = threadIdx.x; e < nobody; e += blockDim.x) {
+  for (uint64_t e = threadIdx.x; e < nobody; e += 256) {
     const uint64_t at = e < before ? e : e - before + (uint64_t)hi * a.q_heads;
     if (a.splits > 1) {
       a.part[a.splits * all * D + (blockIdx.x * all + at) * 2 + 1] = kNothing;
@@ -484,22 +486,23 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, f32x4 o, float
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
-// The most waves of a block: what a CU's registers hold.
-constexpr uint32_t most_waves(int nb, int nq) { return 4 * (nq == 1 ? (nb == 2 ? 4 : nb == 4 ? 3 : 2) : nb < 8 ? 2 : 1); }
+// Blocks of four waves that a CU's registers hold.
+constexpr int at_once(int dim, int nq) { return nq == 1 ? (dim == 64 ? 4 : dim == 128 ? 3 : 2) : dim < 256 ? 2 : 1; }
 
 // A row's output: element 4 d + r of the lane (o[n][d][r]) is dimension 2 NB (4 g + r) + d.
 template <int NB, int NQ, bool F16>
-__global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendArgs a) {
-  constexpr int D = 32 * NB, kWaves = most_waves(NB, NQ);
+__global__ void __launch_bounds__(256, at_once(32 * NB, NQ)) k_kv4_attend(AttendArgs a) {
+  constexpr int D = 32 * NB;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t waves = blockDim.x >> 6;
   const uint32_t r16 = lane & 15, g = lane >> 4;
-  const uint32_t b = blockIdx.z, head = blockIdx.y % a.c.heads, q_tile = blockIdx.y / a.c.heads;
+  const uint32_t b = blockIdx.z;
+  uint32_t head = blockIdx.y, q_tile = 0;
+  if (a.q_tiles > 1) q_tile = blockIdx.y / a.c.heads, head = blockIdx.y - q_tile * a.c.heads;
   if (b == a.t.batch) {  // rows of no sequence
     none<D>(a);
     return;
   }
-  int32_t first, n_rows = (int32_t)(a.t.rows / a.t.batch);
+  int32_t first, n_rows = (int32_t)a.rows_each;
   if (a.t.starts) {
     first = max(a.t.starts[b], 0);
     n_rows = max(min(a.t.starts[b + 1], (int32_t)a.t.rows), 0) - first;
@@ -511,14 +514,15 @@ __global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendAr
   const int32_t capacity = (int32_t)(a.t.wide * a.c.page_tokens);
   const int32_t stored = min(len, capacity);
   const int32_t* table = a.t.table + b * a.t.stride;
-  __shared__ float sc[kWaves][16 * NQ], sl[kWaves][16 * NQ];
+  __shared__ float sc[4][16 * NQ], sl[4][16 * NQ];
   __shared__ uint32_t rows_at[16 * NQ];  // of the output
-  __shared__ __align__(16) float so[kWaves][4][D + 4];
+  __shared__ __align__(16) float so[4][16][D + 4];
 
   for (uint32_t row0 = q_tile * (16 * NQ); row0 < all_rows; row0 += a.q_tiles * (16 * NQ)) {
     // positions of the tile's first and last rows
     const uint32_t last_row = min(row0 + 16 * NQ, all_rows) - 1;
-    const int64_t p_lo = (int64_t)len - n_rows + row0 / a.group, p_hi = (int64_t)len - n_rows + last_row / a.group;
+    const int64_t p_lo = (int64_t)len - n_rows + (row0 ? row0 / a.group : 0);
+    const int64_t p_hi = (int64_t)len - n_rows + (last_row + 1 == all_rows ? (uint32_t)n_rows - 1 : last_row / a.group);
     const int32_t hi = (int32_t)min(max(p_hi, (int64_t)-1), (int64_t)capacity - 1);
     // tiles: those of the sinks, then from the window's first on
     int32_t first_tile = 0, sink_tiles = 0, tiles = 0;
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendAr
       tiles = max(hi / 32 - first_tile + 1, 0) + sink_tiles;
     }
     // the block's tiles (the last split takes what is left), which its waves take in turn
-    const int32_t cut = (int32_t)(blockIdx.x * a.chunk), step = (int32_t)waves;
+    const int32_t cut = (int32_t)(blockIdx.x * a.chunk), step = 4;
     const int32_t to = blockIdx.x + 1 == a.splits ? tiles : min(cut + (int32_t)a.chunk, tiles);
     int32_t v = cut + (int32_t)wave;
 
@@ -553,7 +557,9 @@ __global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendAr
     Wave<NB, NQ, F16> w;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const uint32_t r = min(row0 + n * 16 + r16, all_rows - 1), i = r / a.group, hq = head * a.group + (r - i * a.group);
+      const uint32_t r = min(row0 + n * 16 + r16, all_rows - 1);
+      const uint32_t i = a.group == 1 ? r : all_rows <= 1u << 16 ? __umulhi(r, a.per_group) : r / a.group;
+      const uint32_t hq = head * a.group + (r - i * a.group);
       const bool real = row0 + n * 16 + r16 < all_rows;
       w.pos[n] = real ? (int32_t)max((int64_t)len - n_rows + i, (int64_t)-1) : -1;
       const uint16_t* q = a.q + (first + (int64_t)i) * a.q_row + hq * a.q_head + g * (8 * NB);
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendAr
       page1 = page2;
     }
 
-    // the waves' states joined through LDS, four rows at a time
+    // the four waves' states joined through LDS
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       uint32_t seen = w.seen[n];
@@ -598,49 +604,48 @@ __global__ void __launch_bounds__(64 * most_waves(NB, NQ)) k_kv4_attend(AttendAr
     }
     const uint64_t all = (uint64_t)a.t.rows * a.q_heads;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
-      for (uint32_t r4 = 0; r4 < 16 && row0 + n * 16 + r4 < all_rows; r4 += 4) {
-        __syncthreads();
-        if ((r16 & ~3u) == r4) {
+    for (int n = 0; n < NQ; ++n) {
+      const uint32_t left = all_rows - row0;  // rows from the tile's first on
+      if (n * 16u >= left) break;
+      const uint32_t here = min(16u, left - n * 16);
+      if (n) __syncthreads();
+      if (r16 < here) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int d = 0; d < 2 * NB; ++d) so[wave][r16 & 3][2 * NB * (4 * g + r) + d] = w.o[n][d][r];
+          for (int d = 0; d < 2 * NB; d += 4)
+            *reinterpret_cast<f32x4*>(&so[wave][r16][2 * NB * (4 * g + r) + d]) =
+                f32x4{w.o[n][d][r], w.o[n][d + 1][r], w.o[n][d + 2][r], w.o[n][d + 3][r]};
+      }
+      __syncthreads();
+      for (uint32_t e = threadIdx.x; e < here * (D / 4); e += 256) {
+        const uint32_t row = e / (D / 4), d = e % (D / 4) * 4, in = n * 16 + row;
+        const uint64_t at = rows_at[in];
+        float c = -INFINITY, l = 0.f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        bool seen = false;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          seen |= sl[v][in] != kNothing;
+          c = fmaxf(c, has_weight(sl[v][in]) ? sc[v][in] : -INFINITY);
         }
-        __syncthreads();
-        for (uint32_t e = threadIdx.x; e < D; e += blockDim.x) {
-          const uint32_t row = e / (D / 4), d = e % (D / 4) * 4, in = n * 16 + r4 + row;
-          const uint64_t at = rows_at[in];
-          if (at == ~0u) continue;
-          float c = -INFINITY, l = 0.f;
-          f32x4 o = {0.f, 0.f, 0.f, 0.f};
-          bool seen = false;
-          for (uint32_t v4 = 0; v4 < waves; v4 += 4) {  // four at a time: their reads run together
 #pragma unroll
-            for (uint32_t v = v4; v < v4 + 4; ++v) {
-              seen |= sl[v][in] != kNothing;
-              c = fmaxf(c, has_weight(sl[v][in]) ? sc[v][in] : -INFINITY);
-            }
-          }
-          for (uint32_t v4 = 0; v4 < waves; v4 += 4) {
-#pragma unroll
-            for (uint32_t v = v4; v < v4 + 4; ++v) {
-              const bool some = has_weight(sl[v][in]);
-              const float f = some ? __builtin_amdgcn_exp2f(sc[v][in] - c) : 0.f;
-              l += some ? f * sl[v][in] : 0.f;
-              o += f * *reinterpret_cast<const f32x4*>(&so[v][row][d]);  // zero where there is no weight
-            }
-          }
-          if (a.splits == 1) {
-            store_out<F16>(a.o, at * D + d, o, l, seen);
-          } else {
-            *reinterpret_cast<f32x4*>(a.part + (blockIdx.x * all + at) * D + d) = o;
-            if (d == 0)
-              *reinterpret_cast<f32x2*>(a.part + a.splits * all * D + (blockIdx.x * all + at) * 2) =
-                  f32x2{c, seen ? l : kNothing};
-          }
+        for (int v = 0; v < 4; ++v) {
+          const bool some = has_weight(sl[v][in]);
+          const float f = some ? __builtin_amdgcn_exp2f(sc[v][in] - c) : 0.f;
+          l += some ? f * sl[v][in] : 0.f;
+          o += f * *reinterpret_cast<const f32x4*>(&so[v][row][d]);  // zero where there is no weight
+        }
+        if (a.splits == 1) {
+          store_out<F16>(a.o, at * D + d, o, l, seen);
+        } else {
+          *reinterpret_cast<f32x4*>(a.part + (blockIdx.x * all + at) * D + d) = o;
+          if (d == 0)
+            *reinterpret_cast<f32x2*>(a.part + a.splits * all * D + (blockIdx.x * all + at) * 2) =
+                f32x2{c, seen ? l : kNothing};
         }
       }
+    }
     __syncthreads();
   }
 }
@@ -735,13 +740,12 @@ bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
   return n >> 31 == 0;
 }
 
-constexpr uint64_t kChunk = 8;   // tiles of 32 tokens of a split at least, for its four waves
-constexpr uint64_t kAlone = 1;   // tiles a wave up to which one block takes a sequence
+constexpr uint64_t kChunk = 12;  // tiles of 32 tokens of a split at least, for its four waves
 
 // How an attention call is cut up: query tiles of 16 nq rows, and splits of each
 // sequence's tokens.
 struct Plan {
-  uint32_t nq, q_tiles, waves, splits, chunk;
+  uint32_t nq, q_tiles, splits, chunk;
 };
 
 Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
@@ -760,19 +764,13 @@ Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* a
     if (seen < len) len = seen;
   }
   const uint64_t tiles = (len + 31) / 32 + 1, blocks = (uint64_t)p.q_tiles * c->kv_heads * r->batch;
-  const uint32_t most_w = most_waves((int)c->head_dim / 32, (int)p.nq);
-  uint64_t splits = 1;
-  if (tiles <= kAlone * most_w) {
-    p.waves = tiles > 2 * 4 ? (uint32_t)(tiles / 2 + 3) / 4 * 4 : 4;
-    if (p.waves > most_w) p.waves = most_w;
-  } else {
-    p.waves = 4;
-    splits = 64 * most_w / blocks;
-    const uint64_t top = (tiles + kChunk - 1) / kChunk;
-    if (splits > top) splits = top;
-    if (splits > kMostSplits) splits = kMostSplits;
-    if (splits < 1) splits = 1;
-  }
+  // as many blocks as the card holds at once, and no second round of them: 32 sequences of
+  // up to 32768 tokens take 209 us at 3 splits of each, 233 at 4
+  uint64_t splits = 256 * at_once((int)c->head_dim, (int)p.nq) / blocks;
+  const uint64_t top = (tiles + kChunk - 1) / kChunk;
+  if (splits > top) splits = top;
+  if (splits > kMostSplits) splits = kMostSplits;
+  if (splits < 1) splits = 1;
   p.chunk = (uint32_t)((tiles + splits - 1) / splits);
   p.splits = (uint32_t)((tiles + p.chunk - 1) / p.chunk);
   return p;
@@ -796,17 +794,17 @@ uint64_t part_bytes(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_atten
 }
 
 template <int NB, int NQ, bool F16>
-void launch_attend(hipStream_t stream, const AttendArgs& a, uint32_t waves) {
+void launch_attend(hipStream_t stream, const AttendArgs& a) {
   const uint32_t z = a.t.batch + (a.t.starts ? 1 : 0);
-  hipLaunchKernelGGL((k_kv4_attend<NB, NQ, F16>), dim3(a.splits, a.q_tiles * a.c.heads, z), dim3(64 * waves), 0, stream, a);
+  hipLaunchKernelGGL((k_kv4_attend<NB, NQ, F16>), dim3(a.splits, a.q_tiles * a.c.heads, z), dim3(256), 0, stream, a);
 }
 
 template <int NB, bool F16>
 ecw_status launch_all(hipStream_t stream, const AttendArgs& a, const Plan& p) {
   if (p.nq == 1)
-    launch_attend<NB, 1, F16>(stream, a, p.waves);
+    launch_attend<NB, 1, F16>(stream, a);
   else
-    launch_attend<NB, 2, F16>(stream, a, p.waves);
+    launch_attend<NB, 2, F16>(stream, a);
   if (ecw_status s = launched("kv4_attend")) return s;
   if (a.splits == 1) return ECW_OK;
   const uint64_t all = (uint64_t)a.t.rows * a.q_heads, grid = (all + 3) / 4;
@@ -907,6 +905,8 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
   a.q_tiles = p.q_tiles;
   a.splits = p.splits;
   a.chunk = p.chunk;
+  a.rows_each = rows->rows / rows->batch;
+  a.per_group = (uint32_t)(((uint64_t(1) << 32) + a.group - 1) / a.group);  // unused for one
   const uint32_t page_tiles = cache->page_tokens / 32;
   a.per_page = page_tiles == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + page_tiles - 1) / page_tiles);
   a.window = (int32_t)at->window;
