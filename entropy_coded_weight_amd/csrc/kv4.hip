@@ -52,11 +52,12 @@ __device__ __forceinline__ bool find_row(const Batch& t, uint32_t row, uint32_t*
     else
       hi = mid;
   }
-  const int32_t first = t.starts[lo], end = t.starts[lo + 1];
+  const int32_t first = t.starts[lo], end = min(t.starts[lo + 1], (int32_t)t.rows);
+  if (first < 0 || (int32_t)row < first || (int32_t)row >= end) return false;
   *b = lo;
   *n = end - first;
   *i = (int32_t)row - first;
-  return first >= 0 && (int32_t)row >= first && (int32_t)row < end;
+  return true;
 }
 
 // The page region of a row's token and the token's place in it; null: it has none.

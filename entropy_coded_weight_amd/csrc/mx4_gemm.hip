@@ -650,14 +650,18 @@ ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   while (waves < kFewWaves && (pairs > waves * kTurns || ((uint64_t)nt * waves < 2048 && waves < pairs))) waves *= 2;
   const uint32_t lds = waves * kTurns * kTurnBytes;
   auto* fn = k_mx4_gemm_few<ACT, VEC>;
-  static std::atomic<bool> allowed{false};  // more than 64 KiB of LDS, once
-  if (lds > 64 * 1024 && !allowed.load(std::memory_order_relaxed)) {
-    if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
-                            160 * 1024) != hipSuccess) {
-      (void)hipGetLastError();
-      return refuse(ECW_E_HIP, "hipFuncSetAttribute failed");
+  if (lds > 64 * 1024) {  // to be allowed once on each device
+    static std::atomic<uint64_t> allowed{0};
+    int device = 0;
+    const bool known = hipGetDevice(&device) == hipSuccess && device >= 0 && device < 64;
+    if (!known || !(allowed.load(std::memory_order_relaxed) >> device & 1)) {
+      if (hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              160 * 1024) != hipSuccess) {
+        (void)hipGetLastError();
+        return refuse(ECW_E_HIP, "hipFuncSetAttribute failed");
+      }
+      if (known) allowed.fetch_or(uint64_t(1) << device, std::memory_order_relaxed);
     }
-    allowed.store(true, std::memory_order_relaxed);
   }
   hipLaunchKernelGGL(fn, dim3(nt), dim3(waves * 64), lds, stream, a, y_dtype);
   return launched("mx4_gemm");

@@ -179,6 +179,35 @@ def test_long_sequences_are_split_and_joined(dim, n):
     bed.check(bed.cache.attend(q, bed.table, I32(bed.lens), window=1000, sinks=9), q, [n, n], 1000, 9)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim,group,rows", [(64, 8, [23, 1, 70, 0, 300]), (128, 4, [500, 3, 49, 1, 200]),
+                                            (128, 1, [700, 600, 190, 1, 255]), (64, 1, [256, 257, 31, 33, 512])])
+def test_many_rows(dim, group, rows, dtype):
+    _say("attend many", dim, group, rows, dtype)
+    lens = [n + extra for n, extra in zip(rows, (0, 900, 31, 5, 700))]
+    bed = Bed(lens, 2, dim, dtype=dtype, gone=[(4, 3), (4, 4), (4, 5)])
+    starts = np.concatenate([[0], np.cumsum(rows)])
+    q = _normal(82, sum(rows) + 3, 2 * group, dim, dtype=dtype)  # three rows of nobody
+    for window, sinks in ((0, 0), (70, 33)):
+        o = bed.cache.attend(q, bed.table, I32(lens), starts=I32(starts.tolist()), max_rows=700, window=window,
+                             sinks=sinks)
+        rest = bed.check(o, q, rows, window, sinks)
+        assert not rest.any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_rows_and_bad_values(dim):
+    _say("attend many NaN", dim)
+    k, v = [_normal(1, 500, 1, dim)], [_normal(2, 500, 1, dim)]
+    v[0][433, 0, 40] = float("nan")
+    v[0][460, 0, 3] = float("inf")
+    k[0][480, 0, 0] = float("nan")
+    bed = Bed([500], 1, dim, k=k, v=v)
+    q = _normal(81, 300, 1, dim)
+    bed.check(bed.cache.attend(q, bed.table, I32([500])), q, [300])
+    bed.check(bed.cache.attend(q, bed.table, I32([500]), window=20), q, [300], 20)
+
+
 @pytest.mark.parametrize("page", [32, 96, 128, 416, 4096])
 @pytest.mark.parametrize("n", [1, 20])
 def test_page_sizes(page, n):
