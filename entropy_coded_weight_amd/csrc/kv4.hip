@@ -82,12 +82,12 @@ __device__ __forceinline__ uint32_t value_at(uint32_t nb, uint32_t token, uint32
 }
 
 template <int DT>
-__device__ __forceinline__ uint32_t quantise_row(const void* x, int64_t at, uint32_t u, uint32_t dim, bool vec,
+__device__ __forceinline__ uint32_t quantise_row(const void* x, int64_t at, uint32_t u, uint32_t dim,
                                                  uint32_t* byte) {
   if constexpr (DT == ECW_DT_F32)
-    return quantise_oct(load_oct32(static_cast<const float*>(x) + at, u * 8, dim, vec), byte);
+    return quantise_oct(load_oct32(static_cast<const float*>(x) + at, u * 8, dim), byte);
   else
-    return quantise_oct<DT == ECW_DT_F16>(load_oct16(static_cast<const uint16_t*>(x) + at, u * 8, dim, vec), byte);
+    return quantise_oct<DT == ECW_DT_F16>(load_oct16(static_cast<const uint16_t*>(x) + at, u * 8, dim), byte);
 }
 
 // A lane per 8 dimensions of one head of one row, keys and values both.  Bound by
@@ -95,7 +95,7 @@ __device__ __forceinline__ uint32_t quantise_row(const void* x, int64_t at, uint
 template <int DT>
 __global__ void __launch_bounds__(256) k_kv4_append(Cache c, Batch t, const void* __restrict__ k,
                                                     const void* __restrict__ v, int64_t k_row, int64_t k_head,
-                                                    int64_t v_row, int64_t v_head, bool k_vec, bool v_vec) {
+                                                    int64_t v_row, int64_t v_head) {
   const uint32_t octs = c.dim / 8, nb = c.dim / 32;
   const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
   const uint32_t u = (uint32_t)(id % octs);
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(256) k_kv4_append(Cache c, Batch t, const void
   const uint32_t row = (uint32_t)(rh / c.heads), head = (uint32_t)(rh - (uint64_t)row * c.heads);
   if (row >= t.rows) return;  // whole blocks: a head's lanes stay together
   uint32_t kb, vb, at = 0;
-  const uint32_t kc = quantise_row<DT>(k, row * k_row + head * k_head, u, c.dim, k_vec, &kb);
-  const uint32_t vc = quantise_row<DT>(v, row * v_row + head * v_head, u, c.dim, v_vec, &vb);
+  const uint32_t kc = quantise_row<DT>(k, row * k_row + head * k_head, u, c.dim, &kb);
+  const uint32_t vc = quantise_row<DT>(v, row * v_row + head * v_head, u, c.dim, &vb);
   uint8_t* to = place(c, t, row, head, &at);
   if (!to) return;
   *reinterpret_cast<uint32_t*>(to + (uint64_t)at * (c.dim / 2) + u * 4) = kc;
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __rest
     kb = s[at * nb + u / 4];
     vb = s[scale_bytes(c) + (at / 4 * nb + u / 4) * 4 + at % 4];
   }
-  store_oct<DT>(k, id * 8, kc, scale_of(kb), 8, true);
-  store_oct<DT>(v, id * 8, vc, scale_of(vb), 8, true);
+  store_oct<DT>(k, id * 8, kc, scale_of(kb), 8);
+  store_oct<DT>(v, id * 8, vc, scale_of(vb), 8);
 }
 
 // ------------------------------------------------------------------ attention
@@ -177,7 +177,6 @@ struct AttendArgs {
   uint32_t per_page;      // 2^32 / tiles of a page, rounded up; 0 for one
   int32_t window, sinks;  // window 0: none
   float scale;            // times log2 e
-  bool vec;
 };
 
 // A row's softmax state: its offset and sum.  kNothing as the sum: no token was visible,
@@ -564,13 +563,8 @@ __global__ void __launch_bounds__(256, at_once(32 * NB, NQ)) k_kv4_attend(Attend
       const bool real = row0 + n * 16 + r16 < all_rows;
       w.pos[n] = real ? (int32_t)max((int64_t)len - n_rows + i, (int64_t)-1) : -1;
       const uint16_t* q = a.q + (first + (int64_t)i) * a.q_row + hq * a.q_head + g * (8 * NB);
-      if (a.vec) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) w.q[n][j] = reinterpret_cast<const u32x4*>(q)[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < NB; ++j) w.q[n][j] = load_oct16(q, j * 8, D, false).v;
-      }
+      for (int j = 0; j < NB; ++j) w.q[n][j] = reinterpret_cast<const Loose16*>(q + j * 8)->v;
       if (wave == 0 && g == 0) rows_at[n * 16 + r16] = real ? (first + i) * a.q_heads + hq : ~0u;
       w.c[n] = 0.f;
       w.most[n] = -INFINITY;
@@ -847,13 +841,11 @@ ecw_status kv4_append(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
     if (strides[i] < 0) return refuse(ECW_E_INVALID_ARG, "strides must not be negative");
   uint32_t grid;
   if (!row_grid(cache, rows, &grid)) return refuse(ECW_E_UNSUPPORTED, "too many rows for one launch");
-  const bool kv = aligned(k, 16) && strides[0] * size % 16 == 0 && strides[1] * size % 16 == 0;
-  const bool vv = aligned(v, 16) && strides[2] * size % 16 == 0 && strides[3] * size % 16 == 0;
   auto* fn = dtype == ECW_DT_F32   ? k_kv4_append<ECW_DT_F32>
              : dtype == ECW_DT_F16 ? k_kv4_append<ECW_DT_F16>
                                    : k_kv4_append<ECW_DT_BF16>;
   hipLaunchKernelGGL(fn, dim3(grid), dim3(256), 0, (hipStream_t)stream, cache_of(cache), batch_of(rows), k, v,
-                     strides[0], strides[1], strides[2], strides[3], kv, vv);
+                     strides[0], strides[1], strides[2], strides[3]);
   return launched("kv4_append");
 }
 
@@ -913,7 +905,6 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
   a.window = (int32_t)at->window;
   a.sinks = (int32_t)at->sinks;
   a.scale = at->scale * 1.44269504088896f;
-  a.vec = aligned(q, 16) && q_row % 8 == 0 && q_head % 8 == 0;
   return dtype == ECW_DT_F16 ? launch_dim<true>((hipStream_t)stream, a, p)
                              : launch_dim<false>((hipStream_t)stream, a, p);
 }

@@ -69,15 +69,24 @@ __device__ __forceinline__ void split_f16(u32x4 v, bf16x8* hi, bf16x8* lo) {
   *lo = __builtin_bit_cast(bf16x8, l);
 }
 
-// Eight elements of an input row from column c on, zero from `cols` on.  vec: the row's
-// start and the column are 16-byte aligned.
+// 16 bytes at any multiple of an element: memory instructions take them whole where rows
+// are not 16-byte aligned too (a row of odd length in single elements costs 2 to 15 times
+// the time).
+struct __attribute__((packed, aligned(2))) Loose16 {
+  u32x4 v;
+};
+struct __attribute__((packed, aligned(4))) Loose32 {
+  f32x4 v;
+};
+
+// Eight elements of an input row from column c on, zero from `cols` on.
 struct Oct16 {
   u32x4 v;
 };
-__device__ __forceinline__ Oct16 load_oct16(const uint16_t* row, uint32_t c, uint32_t cols, bool vec) {
+__device__ __forceinline__ Oct16 load_oct16(const uint16_t* row, uint32_t c, uint32_t cols) {
   Oct16 r;
-  if (vec && c + 8 <= cols) {
-    r.v = *reinterpret_cast<const u32x4*>(row + c);
+  if (c + 8 <= cols) {
+    r.v = reinterpret_cast<const Loose16*>(row + c)->v;
     return r;
   }
   uint32_t e[8];
@@ -89,11 +98,11 @@ __device__ __forceinline__ Oct16 load_oct16(const uint16_t* row, uint32_t c, uin
 struct Oct32 {
   f32x4 a, b;
 };
-__device__ __forceinline__ Oct32 load_oct32(const float* row, uint32_t c, uint32_t cols, bool vec) {
+__device__ __forceinline__ Oct32 load_oct32(const float* row, uint32_t c, uint32_t cols) {
   Oct32 r;
-  if (vec && c + 8 <= cols) {
-    r.a = *reinterpret_cast<const f32x4*>(row + c);
-    r.b = *reinterpret_cast<const f32x4*>(row + c + 4);
+  if (c + 8 <= cols) {
+    r.a = reinterpret_cast<const Loose32*>(row + c)->v;
+    r.b = reinterpret_cast<const Loose32*>(row + c + 4)->v;
     return r;
   }
 #pragma unroll
@@ -158,18 +167,18 @@ __device__ __forceinline__ uint32_t quantise_oct(const Oct32& x, uint32_t* byte)
 }
 
 // Eight elements of one block to memory as DT (ECW_DT_F16, _BF16 or _F32), the first
-// `n` of them; vec: 8 of them and the address is 16-byte aligned.
+// `n` of them.
 template <int DT>
-__device__ __forceinline__ void store_oct(void* out, uint64_t at, uint32_t codes, float scale, uint32_t n, bool vec) {
+__device__ __forceinline__ void store_oct(void* out, uint64_t at, uint32_t codes, float scale, uint32_t n) {
   if constexpr (DT == ECW_DT_F32) {
     float* o = static_cast<float*>(out) + at;
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 0);
     const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 1);
     const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 2);
     const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, 3);
-    if (vec && n >= 8) {
-      reinterpret_cast<f32x4*>(o)[0] = f32x4{a[0], a[1], b[0], b[1]};
-      reinterpret_cast<f32x4*>(o)[1] = f32x4{c[0], c[1], d[0], d[1]};
+    if (n >= 8) {
+      reinterpret_cast<Loose32*>(o)[0].v = f32x4{a[0], a[1], b[0], b[1]};
+      reinterpret_cast<Loose32*>(o)[1].v = f32x4{c[0], c[1], d[0], d[1]};
       return;
     }
     const float v[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
@@ -183,8 +192,8 @@ __device__ __forceinline__ void store_oct(void* out, uint64_t at, uint32_t codes
       v = __builtin_bit_cast(u32x4, oct_f16(codes, scale));
     else
       v = __builtin_bit_cast(u32x4, oct_bf16(codes, scale));
-    if (vec && n >= 8) {
-      *reinterpret_cast<u32x4*>(o) = v;
+    if (n >= 8) {
+      reinterpret_cast<Loose16*>(o)->v = v;
       return;
     }
 #pragma unroll

@@ -30,7 +30,6 @@ struct GemmArgs {
   int64_t x_stride;       // elements (16-bit x)
   uint32_t rows, cols, batch;
   uint32_t blocks, scales;  // of a padded row: blocks of codes, bytes of scales
-  bool vec;               // rows of x are 16-byte aligned
 };
 
 template <int DT>
@@ -147,6 +146,15 @@ __device__ __forceinline__ void wait_copies() {
 
 __device__ const u32x4 zeros16 = {0, 0, 0, 0};
 
+// Eight elements of a row of x from column c on come from column min(c, cols - 8), so that
+// they lie in the row wherever it starts and ends; in a row's last span they are moved
+// down by what is too much, with zeros behind them.
+__device__ __forceinline__ uint32_t within(uint32_t c, uint32_t cols) { return min(c, cols - 8); }
+__device__ __forceinline__ u32x4 moved_down(u32x4 v, uint32_t elements) {
+  const unsigned __int128 t = __builtin_bit_cast(unsigned __int128, v);
+  return __builtin_bit_cast(u32x4, elements < 8 ? t >> (16 * elements) : (unsigned __int128)0);
+}
+
 // ------------------------------------------------------------------ a few rows
 // A block computes 16 rows of w times up to 16 rows of x; its waves take pairs of spans in
 // turn and join their sums through LDS, in the order of the waves.  A wave copies w for up
@@ -162,8 +170,9 @@ constexpr uint32_t kTurns = 4;             // pairs of spans that a wave has in 
 constexpr uint32_t kTurnBytes = 16 * 128;  // 16 rows of w
 constexpr uint32_t kFewWaves = 16;         // at most
 
-// VEC: rows of 16-bit x are 16-byte aligned, a multiple of 8 columns, and end within 2^31 bytes.
-template <int ACT, bool VEC>
+// NEAR: 16-bit x ends within 2^31 bytes.  Its rows may start at any element (one row by
+// 14336 x 4095: 10.3 us).
+template <int ACT, bool NEAR>
 __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int y_dtype) {
   extern __shared__ __align__(16) uint8_t lds[];  // each wave's turns, then (over them) the sums
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int
   const uint8_t* xrow = static_cast<const uint8_t*>(a.x) + (ACT == kActMX4 ? m * a.blocks * 16 : (int64_t)m * a.x_stride * 2);
   const uint8_t* xs = ACT == kActMX4 ? a.xs + m * a.scales : nullptr;
   constexpr int kWords = ACT == kActMX4 ? 1 : 4;
-  // 16-bit x as a buffer of bytes: what is past its end, columns or rows, reads as zero
+  // 16-bit x as a buffer of bytes: what is past its end, rows there are not, reads as zero
   // and fetches nothing
   const auto xbuf = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(a.x), 0,
                                                       (uint32_t)(((a.batch - 1) * a.x_stride + a.cols) * 2), 0x00027000);
@@ -195,23 +204,21 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int
     u32x4 x[1][kWords];
     uint32_t sx;
   };
-  // the operands of x in span s (in the last span past the end)
+  // the operands of x in span s; past the last span nothing is fetched, or the last again
   auto load_x = [&](Span& to, uint32_t s) {
+    const uint32_t row = s < spans ? xoff : 1u << 31;
     s = min(s, spans - 1);
     if constexpr (ACT == kActMX4) {
       to.x[0][0] = *reinterpret_cast<const u32x4*>(xrow + (uint64_t)s * 64 + g * 16);
       to.sx = *reinterpret_cast<const uint32_t*>(xs + s * 4);
     } else {
-      const uint16_t* row = reinterpret_cast<const uint16_t*>(xrow);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t c = s * 128 + g * 32 + j * 8;
-        if constexpr (VEC) {
-          to.x[0][j] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, c < a.cols ? xoff + c * 2 : ~0u, 0, 0));
-        } else {
-          to.x[0][j] = load_oct16(row, c, a.cols, false).v;
-        }
+        const uint32_t c = within(s * 128 + g * 32 + j * 8, a.cols);
+        if constexpr (NEAR)
+          to.x[0][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, row + c * 2, 0, 0));
+        else
+          to.x[0][j] = reinterpret_cast<const Loose16*>(xrow + (uint64_t)c * 2)->v;
       }
     }
   };
@@ -248,10 +255,18 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int
         const u32x4 wv = *reinterpret_cast<const u32x4*>(lds + (wave * kTurns + k) * kTurnBytes + r16 * 128 +
                                                          ((h * 4 + g) ^ stirred(r16)) * 16);
         if (s < spans) {
-          if constexpr (ACT == kActMX4)
+          if constexpr (ACT == kActMX4) {
             acc[0] = span_product_mx4(acc[0], wv, sw[k][h], g, now.x[0][0], now.sx);
-          else
+          } else {
+            if (s + 1 == spans) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t c = s * 128 + g * 32 + j * 8;
+                now.x[0][j] = moved_down(now.x[0][j], c - within(c, a.cols));
+              }
+            }
             span_product<ACT, 1>(acc, wv, sw[k][h], g, now.x);
+          }
         }
         if (k + 1 < kTurns) load_x(now, (first + (k + 1) * waves) * 2 + h);
       }
@@ -275,6 +290,27 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int
   }
 }
 
+// Rows of less than 8 columns: an output per lane.
+template <int ACT>
+__global__ void __launch_bounds__(256) k_mx4_gemm_narrow(GemmArgs a, int y_dtype) {
+  const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x, b = at / a.rows, n = at - b * a.rows;
+  if (b >= a.batch) return;
+  const bf16x8 w = oct_bf16(*reinterpret_cast<const uint32_t*>(a.w + n * a.blocks * 16), scale_of(a.ws[n * a.scales]));
+  const int64_t row = (int64_t)b * a.x_stride;
+  float sum = 0.f;
+#pragma unroll
+  for (uint32_t c = 0; c < 7; ++c) {
+    if (c >= a.cols) break;
+    float x;
+    if constexpr (ACT == ECW_DT_F16)
+      x = (float)static_cast<const _Float16*>(a.x)[row + c];
+    else
+      x = (float)static_cast<const __bf16*>(a.x)[row + c];
+    sum = fmaf(x, (float)w[c], sum);
+  }
+  with_type(y_dtype, [&](auto dt) { store_y<dt.value>(a.y, at, sum); });
+}
+
 // ------------------------------------------------------------------ many rows
 // A block's place among the tiles: blocks go to the 8 dies in turn, so each die takes a
 // contiguous run of tiles, and within it 8 tiles of x rows stand next to each other, for
@@ -294,94 +330,6 @@ __device__ __forceinline__ void tile_of(uint32_t m_tiles, uint32_t n_tiles, uint
 // a bank twice (LDS serves lanes 0-3, 12-15 and 20-27 of a wave together).
 __device__ __forceinline__ uint32_t turned(uint32_t o) { return (o & 3) * 4 + (o >> 2); }
 
-// For x whose rows are not 16-byte aligned: 128 rows of x by 128 rows of w per block, 64
-// by 64 per wave, x through registers into LDS, w straight into registers.  The next
-// span's loads are in flight while a span is multiplied.
-template <int ACT>
-__global__ void __launch_bounds__(256, 2) k_mx4_gemm_loose(GemmArgs a, uint32_t m_tiles, uint32_t n_tiles, int y_dtype) {
-  __shared__ u32x4 lds[2][128 * 16];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t r16 = lane & 15, g = lane >> 4;
-  uint32_t mt, nt;
-  tile_of(m_tiles, n_tiles, &mt, &nt);
-  const uint32_t m0 = mt * 128, n0 = nt * 128 + (wave & 1) * 64, mw = (wave >> 1) * 64;
-  const uint32_t spans = a.blocks / 4;
-
-  // this thread's part of an x span: one octet of rows threadIdx / 16 + 16 i
-  const uint32_t oct = turned(threadIdx.x & 15), row = threadIdx.x >> 4;
-  const uint16_t* x[8];
-  u32x4 xs[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = static_cast<const uint16_t*>(a.x) + (int64_t)min(m0 + row + 16 * i, a.batch - 1) * a.x_stride;
-  const uint8_t* w[4];
-  const uint8_t* ws[4];
-  u32x4 wv[4];
-  uint32_t sw[4];
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const uint32_t at = min(n0 + n * 16 + r16, a.rows - 1);
-    w[n] = a.w + (uint64_t)at * a.blocks * 16 + g * 16;
-    ws[n] = a.ws + (uint64_t)at * a.scales;
-  }
-  auto load_x = [&](uint32_t s) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) xs[i] = load_oct16(x[i], s * 128 + oct * 8, a.cols, a.vec).v;
-  };
-  auto load_w = [&](uint32_t s) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      wv[n] = *reinterpret_cast<const u32x4*>(w[n] + (uint64_t)s * 64);
-      sw[n] = *reinterpret_cast<const uint32_t*>(ws[n] + s * 4);
-    }
-  };
-  auto store_x = [&](uint32_t buf) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) lds[buf][(row + 16 * i) * 16 + ((threadIdx.x & 15) ^ row)] = xs[i];
-  };
-
-  f32x4 acc[4][4];  // [n][m]
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-#pragma unroll
-    for (int m = 0; m < 4; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  load_x(0);
-  load_w(0);
-  store_x(0);
-  __syncthreads();
-  for (uint32_t s = 0; s < spans; ++s) {
-    u32x4 wn[4];
-    uint32_t sn[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) wn[n] = wv[n], sn[n] = sw[n];
-    if (s + 1 < spans) {
-      load_x(s + 1);
-      load_w(s + 1);
-    }
-    u32x4 xf[4][4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xf[m][j] = lds[s & 1][(mw + m * 16 + r16) * 16 + ((4 * j + g) ^ r16)];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) span_product<ACT, 4>(acc[n], wn[n], sn[n], g, xf);
-    if (s + 1 < spans) store_x((s + 1) & 1);
-    __syncthreads();
-  }
-  with_type(y_dtype, [&](auto dt) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t b = m0 + mw + m * 16 + g * 4 + r, at = n0 + n * 16 + r16;
-          if (b < a.batch && at < a.rows) store_y<dt.value>(a.y, (uint64_t)b * a.rows + at, acc[n][m][r]);
-        }
-  });
-}
-
 // 16 rows of 4 bits of a span are 1 KiB in LDS: row r's block b at place 4 r + (b ^
 // shifted(r)), so that four neighbouring lanes copy 64 neighbouring bytes and the 16
 // lanes that LDS serves together meet no bank twice.
@@ -391,7 +339,10 @@ __device__ __forceinline__ uint32_t shifted(uint32_t r) { return (0u - (r >> 2))
 // at a time, from NS stages in LDS that copies fill ahead.  EARLY: a wave reads a span's
 // operands from LDS while it multiplies the span before.  Scales come for four spans at
 // once, into places of their own.
-template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY>
+//
+// AHEAD: 0, or rows of x start at any element, which copies cannot: they come through
+// registers, asked for AHEAD spans before they are written to LDS.
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, int AHEAD>
 struct Tiles {
   static constexpr bool kX4 = ACT == kActMX4;
   static constexpr int kWaves = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
@@ -447,10 +398,10 @@ __device__ __forceinline__ void store_run(void* y, uint64_t at, const float (&v)
     if ((uint32_t)i < left) store_y<DT>(y, at + i, v[i]);
 }
 
-template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY>
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, int AHEAD>
 __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint32_t m_tiles, uint32_t n_tiles,
                                                                 int y_dtype) {
-  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY>;
+  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY, AHEAD>;
   __shared__ __align__(16) uint8_t lds[T::kBytes];
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -468,7 +419,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       xp[i] = static_cast<const uint8_t*>(a.x) + (uint64_t)min(m0 + part * 16 + r4, a.batch - 1) * a.blocks * 16 + b4 * 16;
     } else {
       const uint32_t row = part * 4 + g;
-      const uint32_t oct = turned(r16 ^ (row & 15));
+      const uint32_t oct = AHEAD ? 0 : turned(r16 ^ (row & 15));
       xp[i] = static_cast<const uint8_t*>(a.x) + (int64_t)min(m0 + row, a.batch - 1) * a.x_stride * 2 + oct * 16;
     }
   }
@@ -487,9 +438,19 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       sp[i] = a.ws + (uint64_t)min(n0 + row - (T::kX4 ? T::BM : 0), a.rows - 1) * a.scales;
   }
 
+  u32x4 xr[AHEAD ? AHEAD : 1][AHEAD ? T::kXLoads : 1];
+  auto column = [&](uint32_t span, int i) {
+    return span * 128 + turned(r16 ^ (((wave * T::kXLoads + i) * 4 + g) & 15)) * 8;
+  };
+  auto ask = [&](u32x4 (&to)[AHEAD ? T::kXLoads : 1], uint32_t span) {
+#pragma unroll
+    for (int i = 0; i < T::kXLoads; ++i)
+      to[i] = reinterpret_cast<const Loose16*>(xp[i] + (uint64_t)within(column(min(span, spans - 1), i), a.cols) * 2)->v;
+  };
+
   // copies of one span into a stage; past the last span the last one again, into a stage
   // that nothing reads, so that every turn waits for the same number
-  auto fill = [&](uint32_t span, uint32_t stage) {
+  auto fill = [&](uint32_t span, uint32_t stage, auto& held) {
     const uint64_t s = min(span, spans - 1);
     if (span % 4 == 0 && span < spans) {
 #pragma unroll
@@ -500,8 +461,17 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       }
     }
     const uint32_t to = base + stage * T::kStage;
+    if constexpr (AHEAD > 0) {
 #pragma unroll
-    for (int i = 0; i < T::kXLoads; ++i) {
+      for (int i = 0; i < T::kXLoads; ++i) {
+        u32x4 v = held[i];
+        if (span + 1 == spans) v = moved_down(v, column(span, i) - within(column(span, i), a.cols));
+        reinterpret_cast<u32x4*>(lds + stage * T::kStage)[(wave * T::kXLoads + i) * 64 + lane] = v;
+      }
+      ask(held, span + AHEAD);
+    }
+#pragma unroll
+    for (int i = 0; i < (AHEAD ? 0 : T::kXLoads); ++i) {
       const uint32_t part = wave * T::kXLoads + i;
       const uint8_t* from = xp[i] + s * (T::kX4 ? 64 : 256);
       if constexpr (!T::kX4) {
@@ -561,41 +531,55 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
     }
   };
   constexpr int kCopies = T::kXLoads + T::kWLoads;  // of a span; scales may be among those waited for too
-  uint32_t stage = 0;                               // of the span that is multiplied
+  constexpr int kSets = AHEAD ? AHEAD : 1, kTurn = EARLY && kSets % 2 ? 2 * kSets : kSets;
+  uint32_t stage = 0;  // of the span that is multiplied
+  if constexpr (AHEAD > 0) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) ask(xr[i], i);
+  }
   if constexpr (EARLY) {
-    auto step = [&](uint32_t s, const Operands& now, Operands& next) {
+    auto step = [&](uint32_t s, const Operands& now, Operands& next, auto& held) {
       wait_copies<(NS - 2) * kCopies>();
       __builtin_amdgcn_s_barrier();  // the next span is there, and this one's stage is read
-      fill(s + NS, stage);
+      fill(s + NS, stage, held);
       stage = stage + 1 == NS ? 0 : stage + 1;
       read(next, s + 1, stage);
       __builtin_amdgcn_sched_barrier(0);
       multiply(now);
     };
 #pragma unroll
-    for (int i = 0; i < NS; ++i) fill(i, i);
+    for (int i = 0; i < NS; ++i) fill(i, i, xr[i % kSets]);
     wait_copies<(NS - 1) * kCopies>();
     __builtin_amdgcn_s_barrier();
     Operands even, odd;
     read(even, 0, 0);
-    for (uint32_t s = 0; s < spans; s += 2) {
-      step(s, even, odd);
-      if (s + 1 == spans) break;
-      step(s + 1, odd, even);
+    for (uint32_t s = 0; s < spans; s += kTurn) {
+#pragma unroll
+      for (int i = 0; i < kTurn; ++i) {
+        if (s + i >= spans) break;
+        if (i % 2)
+          step(s + i, odd, even, xr[(i + NS) % kSets]);
+        else
+          step(s + i, even, odd, xr[(i + NS) % kSets]);
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) fill(i, i);
+    for (int i = 0; i < NS - 1; ++i) fill(i, i, xr[i % kSets]);
     uint32_t before = NS - 1;  // the stage of the span before
-    for (uint32_t s = 0; s < spans; ++s) {
-      wait_copies<(NS - 2) * kCopies>();
-      __builtin_amdgcn_s_barrier();  // this span is there, and the one before it is done with
-      fill(s + NS - 1, before);
-      Operands now;
-      read(now, s, stage);
-      multiply(now);
-      before = stage;
-      stage = stage + 1 == NS ? 0 : stage + 1;
+    for (uint32_t s = 0; s < spans; s += kTurn) {
+#pragma unroll
+      for (int i = 0; i < kTurn; ++i) {
+        if (s + i >= spans) break;
+        wait_copies<(NS - 2) * kCopies>();
+        __builtin_amdgcn_s_barrier();  // this span is there, and the one before it is done with
+        fill(s + i + NS - 1, before, xr[(i + NS - 1) % kSets]);
+        Operands now;
+        read(now, s + i, stage);
+        multiply(now);
+        before = stage;
+        stage = stage + 1 == NS ? 0 : stage + 1;
+      }
     }
   }
   wait_copies<0>();
@@ -642,14 +626,14 @@ ecw_status check_weight(const void* codes, const void* scales, uint32_t rows, ui
   return ECW_OK;
 }
 
-template <int ACT, bool VEC>
+template <int ACT, bool NEAR>
 ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   const uint32_t nt = (a.rows + 15) / 16, pairs = (a.blocks / 4 + 1) / 2;
   // up to four pairs a wave, and waves enough to fill the card
   uint32_t waves = 4;
   while (waves < kFewWaves && (pairs > waves * kTurns || ((uint64_t)nt * waves < 2048 && waves < pairs))) waves *= 2;
   const uint32_t lds = waves * kTurns * kTurnBytes;
-  auto* fn = k_mx4_gemm_few<ACT, VEC>;
+  auto* fn = k_mx4_gemm_few<ACT, NEAR>;
   if (lds > 64 * 1024) {  // to be allowed once on each device
     static std::atomic<uint64_t> allowed{0};
     int device = 0;
@@ -671,12 +655,12 @@ uint64_t tiles(const GemmArgs& a, uint32_t bm, uint32_t bn) {
   return (uint64_t)((a.batch + bm - 1) / bm) * ((a.rows + bn - 1) / bn);
 }
 
-template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY>
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, int AHEAD = 0>
 ecw_status launch_tile(hipStream_t stream, const GemmArgs& a, int y_dtype) {
-  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY>;
+  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY, AHEAD>;
   const uint32_t m_tiles = (a.batch + T::BM - 1) / T::BM, n_tiles = (a.rows + T::BN - 1) / T::BN;
   if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
-  hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS, EARLY>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves), 0,
+  hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS, EARLY, AHEAD>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves), 0,
                      stream, a, m_tiles, n_tiles, y_dtype);
   return launched("mx4_gemm");
 }
@@ -691,7 +675,10 @@ ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   // A few rows go a block per 16 rows of w, which reads x once for each: more rows and a
   // short K are better off in tiles (16 rows by 14336 x 4096 22.6 and 13.8 us, 4 rows 14.5;
   // by 4096 x 14336 21.8 and 37.8).
-  const bool few = a.batch <= 4 || (a.batch <= 16 && (tiles(a, 32, 64) < kCus / 2 || a.blocks > 4 * 48));
+  // Operands that start between two words are slow to load (16 rows by 4096 x 14335 54 us,
+  // in tiles 42; 4 rows 21).
+  const bool words = ACT == kActMX4 || (aligned(a.x, 4) && a.x_stride % 2 == 0);
+  const bool few = a.batch <= 4 || (a.batch <= 16 && words && (tiles(a, 32, 64) < kCus / 2 || a.blocks > 4 * 48));
   if constexpr (ACT == kActMX4) {
     if (few) return launch_few<ACT, true>(stream, a, y_dtype);
     if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 5, true>(stream, a, y_dtype);
@@ -699,24 +686,28 @@ ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
     if (tiles(a, 128, 256) <= kCus) return launch_tile<ACT, 2, 4, 4, 4, 4, true>(stream, a, y_dtype);
     return launch_tile<ACT, 2, 4, 8, 4, 3, false>(stream, a, y_dtype);
   } else {
-    const bool vec = a.vec && a.cols % 8 == 0;
-    if (vec) {
-      if (few) {
-        const bool near = ((uint64_t)(a.batch - 1) * (uint64_t)a.x_stride + a.cols) >> 30 == 0;
-        return near ? launch_few<ACT, true>(stream, a, y_dtype) : launch_few<ACT, false>(stream, a, y_dtype);
-      }
+    if (a.cols < 8) {
+      const uint64_t grid = ((uint64_t)a.batch * a.rows + 255) / 256;
+      if (grid >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
+      hipLaunchKernelGGL(k_mx4_gemm_narrow<ACT>, dim3((uint32_t)grid), dim3(256), 0, stream, a, y_dtype);
+      return launched("mx4_gemm");
+    }
+    if (few) {
+      const bool near = ((uint64_t)(a.batch - 1) * (uint64_t)a.x_stride + a.cols) >> 30 == 0;
+      return near ? launch_few<ACT, true>(stream, a, y_dtype) : launch_few<ACT, false>(stream, a, y_dtype);
+    }
+    if (aligned(a.x, 16) && a.x_stride % 8 == 0 && a.cols % 8 == 0) {
       if (a.batch <= 32) return launch_tile<ACT, 1, 4, 2, 1, 5, true>(stream, a, y_dtype);
       if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 4, true>(stream, a, y_dtype);
       if (tiles(a, 64, 128) <= kCus) return launch_tile<ACT, 2, 4, 2, 2, 5, true>(stream, a, y_dtype);
       if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 3, false>(stream, a, y_dtype);
       return launch_tile<ACT, 2, 4, 4, 4, 3, false>(stream, a, y_dtype);
     }
-    if (a.batch <= 16) return launch_few<ACT, false>(stream, a, y_dtype);
-    const uint32_t m_tiles = (a.batch + 127) / 128, n_tiles = (a.rows + 127) / 128;
-    if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
-    hipLaunchKernelGGL(k_mx4_gemm_loose<ACT>, dim3(m_tiles * n_tiles), dim3(256), 0, stream, a, m_tiles, n_tiles,
-                       y_dtype);
-    return launched("mx4_gemm");
+    if (a.batch <= 32) return launch_tile<ACT, 1, 4, 2, 1, 5, true, 4>(stream, a, y_dtype);
+    if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 4, true, 4>(stream, a, y_dtype);
+    if (tiles(a, 64, 128) <= kCus) return launch_tile<ACT, 2, 4, 2, 2, 5, true, 4>(stream, a, y_dtype);
+    if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 3, false, 3>(stream, a, y_dtype);
+    return launch_tile<ACT, 2, 4, 4, 4, 3, false, 2>(stream, a, y_dtype);
   }
 }
 
@@ -743,7 +734,7 @@ ecw_status mx4_gemm(ecw_stream stream, const void* w_codes, const void* w_scales
   if (!x || !aligned(x, 2) || x_stride < 0)
     return refuse(ECW_E_INVALID_ARG, "x must be an aligned device pointer with a row stride of 0 or more");
   const GemmArgs a{static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales), x, nullptr, y,
-                   x_stride, rows, cols, batch, row_blocks(cols), scale_stride(cols), aligned(x, 16) && x_stride % 8 == 0};
+                   x_stride, rows, cols, batch, row_blocks(cols), scale_stride(cols)};
   return x_dtype == ECW_DT_F16 ? launch<ECW_DT_F16>((hipStream_t)stream, a, y_dtype)
                                : launch<ECW_DT_BF16>((hipStream_t)stream, a, y_dtype);
 }
@@ -756,7 +747,7 @@ ecw_status mx4_gemm_mx4(ecw_stream stream, const void* w_codes, const void* w_sc
   if (rows == 0 || batch == 0) return ECW_OK;
   if (ecw_status s = check_output(y, y_dtype, batch)) return s;
   const GemmArgs a{static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales), x_codes,
-                   static_cast<const uint8_t*>(x_scales), y, 0, rows, cols, batch, row_blocks(cols), scale_stride(cols), true};
+                   static_cast<const uint8_t*>(x_scales), y, 0, rows, cols, batch, row_blocks(cols), scale_stride(cols)};
   return launch<kActMX4>((hipStream_t)stream, a, y_dtype);
 }
 

@@ -25,17 +25,16 @@ ecw_status launched(const char* what) noexcept {
 // input in one load and writes 256 bytes of codes.  Bound by memory.
 template <int DT>
 __global__ void __launch_bounds__(256) k_mx4_quantise(const void* __restrict__ x, int64_t stride, uint32_t rows,
-                                                      uint32_t cols, uint32_t octs, bool vec,
-                                                      uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+                                                      uint32_t cols, uint32_t octs, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
   const uint32_t row = (uint32_t)(at / octs), oct = (uint32_t)(at - (uint64_t)row * octs);
   if (row >= rows) return;  // whole blocks: octs is a multiple of 16
   uint32_t c, b;
   if constexpr (DT == ECW_DT_F32)
-    c = quantise_oct(load_oct32(static_cast<const float*>(x) + row * stride, oct * 8, cols, vec), &b);
+    c = quantise_oct(load_oct32(static_cast<const float*>(x) + row * stride, oct * 8, cols), &b);
   else
     c = quantise_oct<DT == ECW_DT_F16>(
-        load_oct16(static_cast<const uint16_t*>(x) + row * stride, oct * 8, cols, vec), &b);
+        load_oct16(static_cast<const uint16_t*>(x) + row * stride, oct * 8, cols), &b);
   codes[at] = c;
   if ((oct & 3) == 0) {
     const uint32_t stride = scale_stride(cols), block = oct >> 2, blocks = octs >> 2;
@@ -49,13 +48,12 @@ __global__ void __launch_bounds__(256) k_mx4_quantise(const void* __restrict__ x
 template <int DT>
 __global__ void __launch_bounds__(256) k_mx4_dequantise(const uint32_t* __restrict__ codes,
                                                         const uint8_t* __restrict__ scales, uint32_t rows,
-                                                        uint32_t cols, uint32_t octs, bool vec,
-                                                        void* __restrict__ out) {
+                                                        uint32_t cols, uint32_t octs, void* __restrict__ out) {
   const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
   const uint32_t row = (uint32_t)(at / octs), oct = (uint32_t)(at - (uint64_t)row * octs);
   if (row >= rows || oct * 8 >= cols) return;
   store_oct<DT>(out, (uint64_t)row * cols + oct * 8, codes[at],
-                scale_of(scales[(uint64_t)row * scale_stride(cols) + (oct >> 2)]), cols - oct * 8, vec);
+                scale_of(scales[(uint64_t)row * scale_stride(cols) + (oct >> 2)]), cols - oct * 8);
 }
 
 }  // namespace ecw
@@ -89,11 +87,10 @@ ecw_status mx4_quantize(ecw_stream stream, const void* x, int x_dtype, int64_t r
   const uint32_t octs = row_blocks(cols) * 4;
   const uint64_t grid = ((uint64_t)rows * octs + 255) / 256;
   if (grid >> 31) return refuse(ECW_E_UNSUPPORTED, "matrix too large for one launch");
-  const bool vec = aligned(x, 16) && row_stride * size % 16 == 0;
   auto* fn = x_dtype == ECW_DT_F32   ? k_mx4_quantise<ECW_DT_F32>
              : x_dtype == ECW_DT_F16 ? k_mx4_quantise<ECW_DT_F16>
                                      : k_mx4_quantise<ECW_DT_BF16>;
-  hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(256), 0, (hipStream_t)stream, x, row_stride, rows, cols, octs, vec,
+  hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(256), 0, (hipStream_t)stream, x, row_stride, rows, cols, octs,
                      static_cast<uint32_t*>(codes), static_cast<uint8_t*>(scales));
   return launched("mx4_quantize");
 }
@@ -109,13 +106,11 @@ ecw_status mx4_dequantize(ecw_stream stream, const void* codes, const void* scal
   const uint32_t octs = row_blocks(cols) * 4;
   const uint64_t grid = ((uint64_t)rows * octs + 255) / 256;
   if (grid >> 31) return refuse(ECW_E_UNSUPPORTED, "matrix too large for one launch");
-  const bool vec = aligned(out, 16) && (uint64_t)cols * size % 16 == 0;
   auto* fn = out_dtype == ECW_DT_F32   ? k_mx4_dequantise<ECW_DT_F32>
              : out_dtype == ECW_DT_F16 ? k_mx4_dequantise<ECW_DT_F16>
                                        : k_mx4_dequantise<ECW_DT_BF16>;
   hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(256), 0, (hipStream_t)stream,
-                     static_cast<const uint32_t*>(codes), static_cast<const uint8_t*>(scales), rows, cols, octs, vec,
-                     out);
+                     static_cast<const uint32_t*>(codes), static_cast<const uint8_t*>(scales), rows, cols, octs, out);
   return launched("mx4_dequantize");
 }
 

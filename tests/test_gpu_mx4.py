@@ -311,3 +311,42 @@ def test_gemm_rows_far_apart():
         x.copy_(_matrix(batch, 96, torch.bfloat16, seed=3, spread=0))
         w = _matrix(50, 96, torch.bfloat16, seed=1, spread=0)
         _check_product(w, x, ecw.mx4_quantize(w).gemm(x))
+
+
+def _loose(batch, cols, stride, dtype):
+    """Rows that start at an odd element, with NaN before, between and behind them."""
+    flat = torch.full((stride * batch + cols + 16,), float("nan"), dtype=dtype, device="cuda")
+    x = flat.as_strided((batch, cols), (stride, 1), 1)
+    return x.copy_(_matrix(batch, cols, dtype, seed=5, spread=0))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("cols", [8, 9, 15, 127, 129, 250, 260, 391, 520, 645, 1151])
+def test_gemm_rows_at_odd_elements(cols, dtype):
+    """Last spans of every kind, and fewer spans than are asked for ahead."""
+    for batch, rows in ((1, 40), (9, 70), (24, 70), (60, 70)):
+        _say("gemm odd rows", batch, rows, cols, dtype)
+        w, x = _matrix(rows, cols, torch.bfloat16, seed=1, spread=1.0), _loose(batch, cols, cols + 2, dtype)
+        _check_product(w, x, ecw.mx4_quantize(w).gemm(x))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("batch,rows,cols", [(40, 16400, 131), (70, 8200, 650), (70, 16400, 397), (200, 8200, 265),
+                                             (200, 8200, 777), (260, 16500, 139), (260, 16500, 1030)])
+def test_gemm_rows_at_odd_elements_every_tile_size(batch, rows, cols, dtype):
+    _say("gemm odd rows, tiles", batch, rows, cols, dtype)
+    w, x = _matrix(rows, cols, torch.bfloat16, seed=1, spread=1.0), _loose(batch, cols, cols, dtype)
+    _check_product(w, x, ecw.mx4_quantize(w).gemm(x))
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("cols", [1, 4, 7])
+def test_gemm_narrow_rows(cols, dtype, out):
+    _say("gemm narrow", cols, dtype, out)
+    w, x = _matrix(300, cols, torch.bfloat16, seed=1, spread=1.0), _loose(33, cols, cols + 1, dtype)
+    w[7, 0] = float("nan")
+    y = ecw.mx4_quantize(w).gemm(x, out_dtype=out)
+    assert y[:, 7].isnan().all()
+    w, y = torch.cat([w[:7], w[8:]]), torch.cat([y[:, :7], y[:, 8:]], 1)
+    _check_product(w, x, y)
