@@ -78,6 +78,9 @@ struct __attribute__((packed, aligned(2))) Loose16 {
 struct __attribute__((packed, aligned(4))) Loose32 {
   f32x4 v;
 };
+struct __attribute__((packed, aligned(4))) Words {
+  u32x4 v;
+};
 
 // Eight elements of an input row from column c on, zero from `cols` on.
 struct Oct16 {

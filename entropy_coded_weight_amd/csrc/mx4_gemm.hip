@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int
   }
 }
 
-// Rows of less than 8 columns: an output per lane.
+// Rows of up to 8 columns: an output per lane.
 template <int ACT>
 __global__ void __launch_bounds__(256) k_mx4_gemm_narrow(GemmArgs a, int y_dtype) {
   const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x, b = at / a.rows, n = at - b * a.rows;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(256) k_mx4_gemm_narrow(GemmArgs a, int y_dtype
   const int64_t row = (int64_t)b * a.x_stride;
   float sum = 0.f;
 #pragma unroll
-  for (uint32_t c = 0; c < 7; ++c) {
+  for (uint32_t c = 0; c < 8; ++c) {
     if (c >= a.cols) break;
     float x;
     if constexpr (ACT == ECW_DT_F16)
@@ -340,20 +340,28 @@ __device__ __forceinline__ uint32_t shifted(uint32_t r) { return (0u - (r >> 2))
 // operands from LDS while it multiplies the span before.  Scales come for four spans at
 // once, into places of their own.
 //
-// AHEAD: 0, or rows of x start at any element, which copies cannot: they come through
-// registers, asked for AHEAD spans before they are written to LDS.
-template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, int AHEAD>
+// LOOSE: rows of x start at any element, which copies cannot: they come through registers,
+// asked for a step before they are written to LDS (more steps gained nothing; bound by
+// loads that no 16 bytes are aligned for: 32 rows by 4096 x 14335 38 us).
+//
+// KG: a block has KG times the waves, which take KG spans at once and add their sums up at
+// the end, in order.  With one wave a SIMD every instruction waits for the one before (64
+// rows by 4096 x 14336 in 64x64 with KG 1 and 2 65 and 42 us, 32 rows in 32x64 with KG 1, 2
+// and 4 42, 28 and 24).
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, bool LOOSE, int KG>
 struct Tiles {
   static constexpr bool kX4 = ACT == kActMX4;
   static constexpr int kWaves = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
-  static constexpr uint32_t kX = kX4 ? BM * 64 : BM * 256, kW = BN * 64, kStage = kX + kW;
+  static constexpr uint32_t kX = kX4 ? BM * 64 : BM * 256, kW = BN * 64, kSpan = kX + kW, kStage = KG * kSpan;
   static constexpr uint32_t kScaleRows = (kX4 ? BM : 0) + BN;  // those of x first
-  static constexpr uint32_t kScalePlaces = (NS + 3) / 4 + 1;
+  static constexpr uint32_t kScalePlaces = (NS * KG + 3) / 4 + 1;
   static constexpr uint32_t kBytes = kStage * NS + kScalePlaces * kScaleRows * 16;
   static constexpr int kXLoads = kX / 1024 / kWaves, kWLoads = kW / 1024 / kWaves;  // copies per wave and span
   static constexpr int kSLoads = (kScaleRows / 64 + kWaves - 1) / kWaves;           // per four spans
   static_assert(kX % (1024 * kWaves) == 0 && kW % (1024 * kWaves) == 0, "");
   static_assert(kBytes <= 160 * 1024, "");
+  static_assert(4 % KG == 0, "");                                            // a step's scales come together
+  static_assert((KG - 1) * kWaves * TM * TN * 1024 <= (int)kStage * NS, "");  // sums of the other groups
 };
 
 // Two 4-bit operands are multiplied the other way round, w's rows down the result's
@@ -398,17 +406,19 @@ __device__ __forceinline__ void store_run(void* y, uint64_t at, const float (&v)
     if ((uint32_t)i < left) store_y<DT>(y, at + i, v[i]);
 }
 
-template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, int AHEAD>
-__global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint32_t m_tiles, uint32_t n_tiles,
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, bool LOOSE, int KG>
+__global__ void __launch_bounds__(64 * WM * WN * KG) k_mx4_gemm_tile(GemmArgs a, uint32_t m_tiles, uint32_t n_tiles,
                                                                 int y_dtype) {
-  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY, AHEAD>;
+  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY, LOOSE, KG>;
   __shared__ __align__(16) uint8_t lds[T::kBytes];
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lane = threadIdx.x & 63, waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t kg = waves / T::kWaves, wave = waves % T::kWaves;
   const uint32_t r16 = lane & 15, g = lane >> 4;
   uint32_t mt, nt;
   tile_of(m_tiles, n_tiles, &mt, &nt);
   const uint32_t m0 = mt * T::BM, n0 = nt * T::BN, spans = a.blocks / 4;
+  const uint32_t steps = (spans + KG - 1) / KG;
 
   const uint8_t *xp[T::kXLoads], *wp[T::kWLoads], *sp[T::kSLoads];
   const uint32_t r4 = lane >> 2, b4 = (lane & 3) ^ shifted(r4);  // row and block that the lane copies of 16 rows
@@ -419,7 +429,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       xp[i] = static_cast<const uint8_t*>(a.x) + (uint64_t)min(m0 + part * 16 + r4, a.batch - 1) * a.blocks * 16 + b4 * 16;
     } else {
       const uint32_t row = part * 4 + g;
-      const uint32_t oct = AHEAD ? 0 : turned(r16 ^ (row & 15));
+      const uint32_t oct = LOOSE ? 0 : turned(r16 ^ (row & 15));
       xp[i] = static_cast<const uint8_t*>(a.x) + (int64_t)min(m0 + row, a.batch - 1) * a.x_stride * 2 + oct * 16;
     }
   }
@@ -438,21 +448,33 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       sp[i] = a.ws + (uint64_t)min(n0 + row - (T::kX4 ? T::BM : 0), a.rows - 1) * a.scales;
   }
 
-  u32x4 xr[AHEAD ? AHEAD : 1][AHEAD ? T::kXLoads : 1];
+  // Rows at an odd element: eight elements from the second on, in whole words, and the
+  // first (16 bytes that start between two words take three times as long).
+  struct Held {
+    u32x4 v;
+    uint32_t first;
+  };
+  Held held[LOOSE ? T::kXLoads : 1];
+  auto odd = [&](int i) { return (uint32_t)(reinterpret_cast<uintptr_t>(xp[i]) >> 1 & 1); };
   auto column = [&](uint32_t span, int i) {
     return span * 128 + turned(r16 ^ (((wave * T::kXLoads + i) * 4 + g) & 15)) * 8;
   };
-  auto ask = [&](u32x4 (&to)[AHEAD ? T::kXLoads : 1], uint32_t span) {
+  auto ask = [&](uint32_t span) {
 #pragma unroll
-    for (int i = 0; i < T::kXLoads; ++i)
-      to[i] = reinterpret_cast<const Loose16*>(xp[i] + (uint64_t)within(column(min(span, spans - 1), i), a.cols) * 2)->v;
+    for (int i = 0; i < T::kXLoads; ++i) {
+      const uint16_t* from = reinterpret_cast<const uint16_t*>(xp[i]) +
+                             within(column(min(span, spans - 1), i), a.cols - odd(i));
+      held[i].first = *from;
+      held[i].v = reinterpret_cast<const Words*>(from + odd(i))->v;
+    }
   };
 
-  // copies of one span into a stage; past the last span the last one again, into a stage
-  // that nothing reads, so that every turn waits for the same number
-  auto fill = [&](uint32_t span, uint32_t stage, auto& held) {
+  // copies of one step's span into a stage; past the last span the last one again, into a
+  // place that is not multiplied, so that every turn waits for the same number
+  auto fill = [&](uint32_t step, uint32_t stage) {
+    const uint32_t span = step * KG + kg;
     const uint64_t s = min(span, spans - 1);
-    if (span % 4 == 0 && span < spans) {
+    if (kg == 0 && span % 4 == 0 && span < spans) {
 #pragma unroll
       for (int i = 0; i < T::kSLoads; ++i) {
         const uint32_t part = wave + i * T::kWaves;
@@ -460,18 +482,23 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
           to_lds<16>(sp[i] + s * 4, base + T::kStage * NS + (span / 4 % T::kScalePlaces) * T::kScaleRows * 16 + part * 1024);
       }
     }
-    const uint32_t to = base + stage * T::kStage;
-    if constexpr (AHEAD > 0) {
+    const uint32_t to = base + stage * T::kStage + kg * T::kSpan;
+    if constexpr (LOOSE) {
 #pragma unroll
       for (int i = 0; i < T::kXLoads; ++i) {
-        u32x4 v = held[i];
-        if (span + 1 == spans) v = moved_down(v, column(span, i) - within(column(span, i), a.cols));
-        reinterpret_cast<u32x4*>(lds + stage * T::kStage)[(wave * T::kXLoads + i) * 64 + lane] = v;
+        u32x4 v = held[i].v;
+        if (odd(i))
+          v = u32x4{held[i].first | v[0] << 16, v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16};
+        if (span + 1 == spans) {
+          const uint32_t more = column(span, i) - within(column(span, i), a.cols - odd(i));
+          if (more) v = moved_down(held[i].v, more - odd(i));
+        }
+        reinterpret_cast<u32x4*>(lds + stage * T::kStage + kg * T::kSpan)[(wave * T::kXLoads + i) * 64 + lane] = v;
       }
-      ask(held, span + AHEAD);
+      ask(span + KG);
     }
 #pragma unroll
-    for (int i = 0; i < (AHEAD ? 0 : T::kXLoads); ++i) {
+    for (int i = 0; i < (LOOSE ? 0 : T::kXLoads); ++i) {
       const uint32_t part = wave * T::kXLoads + i;
       const uint8_t* from = xp[i] + s * (T::kX4 ? 64 : 256);
       if constexpr (!T::kX4) {
@@ -496,8 +523,9 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
     u32x4 x[TM][T::kX4 ? 1 : 4], w[TN];
     uint32_t xs[TM], ws[TN];
   };
-  auto read = [&](Operands& f, uint32_t s, uint32_t stage) {
-    const uint8_t* at = lds + stage * T::kStage;
+  auto read = [&](Operands& f, uint32_t step, uint32_t stage) {
+    const uint32_t s = step * KG + kg;
+    const uint8_t* at = lds + stage * T::kStage + kg * T::kSpan;
     const u32x4* x = reinterpret_cast<const u32x4*>(at);
     const u32x4* w = reinterpret_cast<const u32x4*>(at + T::kX);
     const uint32_t* xs = reinterpret_cast<const uint32_t*>(lds + T::kStage * NS + (s / 4 % T::kScalePlaces) * T::kScaleRows * 16) + s % 4;
@@ -518,7 +546,8 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       }
     }
   };
-  auto multiply = [&](const Operands& f) {
+  auto multiply = [&](const Operands& f, uint32_t step) {
+    if (KG > 1 && step * KG + kg >= spans) return;
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
       if constexpr (T::kX4) {
@@ -530,59 +559,63 @@ __global__ void __launch_bounds__(64 * WM * WN) k_mx4_gemm_tile(GemmArgs a, uint
       }
     }
   };
-  constexpr int kCopies = T::kXLoads + T::kWLoads;  // of a span; scales may be among those waited for too
-  constexpr int kSets = AHEAD ? AHEAD : 1, kTurn = EARLY && kSets % 2 ? 2 * kSets : kSets;
-  uint32_t stage = 0;  // of the span that is multiplied
-  if constexpr (AHEAD > 0) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) ask(xr[i], i);
-  }
+  constexpr int kCopies = T::kXLoads + T::kWLoads;  // of a step; scales may be among those waited for too
+  uint32_t stage = 0;                               // of the step that is multiplied
+  if constexpr (LOOSE) ask(kg);
   if constexpr (EARLY) {
-    auto step = [&](uint32_t s, const Operands& now, Operands& next, auto& held) {
+    auto turn = [&](uint32_t s, const Operands& now, Operands& next) {
       wait_copies<(NS - 2) * kCopies>();
-      __builtin_amdgcn_s_barrier();  // the next span is there, and this one's stage is read
-      fill(s + NS, stage, held);
+      __builtin_amdgcn_s_barrier();  // the next step is there, and this one's stage is read
+      fill(s + NS, stage);
       stage = stage + 1 == NS ? 0 : stage + 1;
       read(next, s + 1, stage);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(now);
+      multiply(now, s);
     };
 #pragma unroll
-    for (int i = 0; i < NS; ++i) fill(i, i, xr[i % kSets]);
+    for (int i = 0; i < NS; ++i) fill(i, i);
     wait_copies<(NS - 1) * kCopies>();
     __builtin_amdgcn_s_barrier();
     Operands even, odd;
     read(even, 0, 0);
-    for (uint32_t s = 0; s < spans; s += kTurn) {
-#pragma unroll
-      for (int i = 0; i < kTurn; ++i) {
-        if (s + i >= spans) break;
-        if (i % 2)
-          step(s + i, odd, even, xr[(i + NS) % kSets]);
-        else
-          step(s + i, even, odd, xr[(i + NS) % kSets]);
-      }
+    for (uint32_t s = 0; s < steps; s += 2) {
+      turn(s, even, odd);
+      if (s + 1 == steps) break;
+      turn(s + 1, odd, even);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) fill(i, i, xr[i % kSets]);
-    uint32_t before = NS - 1;  // the stage of the span before
-    for (uint32_t s = 0; s < spans; s += kTurn) {
-#pragma unroll
-      for (int i = 0; i < kTurn; ++i) {
-        if (s + i >= spans) break;
-        wait_copies<(NS - 2) * kCopies>();
-        __builtin_amdgcn_s_barrier();  // this span is there, and the one before it is done with
-        fill(s + i + NS - 1, before, xr[(i + NS - 1) % kSets]);
-        Operands now;
-        read(now, s + i, stage);
-        multiply(now);
-        before = stage;
-        stage = stage + 1 == NS ? 0 : stage + 1;
-      }
+    for (int i = 0; i < NS - 1; ++i) fill(i, i);
+    uint32_t before = NS - 1;  // the stage of the step before
+    for (uint32_t s = 0; s < steps; ++s) {
+      wait_copies<(NS - 2) * kCopies>();
+      __builtin_amdgcn_s_barrier();  // this step is there, and the one before it is done with
+      fill(s + NS - 1, before);
+      Operands now;
+      read(now, s, stage);
+      multiply(now, s);
+      before = stage;
+      stage = stage + 1 == NS ? 0 : stage + 1;
     }
   }
   wait_copies<0>();
+  if constexpr (KG > 1) {
+    __builtin_amdgcn_s_barrier();  // every wave is done with the stages
+    f32x4* sums = reinterpret_cast<f32x4*>(lds) + wave * TN * TM * 64 + lane;
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+        if (kg > 0) sums[((kg - 1) * T::kWaves * TN * TM + n * TM + m) * 64] = acc[n][m];
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int k = 0; k < KG - 1; ++k)
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[n][m] += sums[(k * T::kWaves * TN * TM + n * TM + m) * 64];
+  }
   with_type(y_dtype, [&](auto dt) {
     if constexpr (T::kX4) {
       const uint32_t at = n0 + wn * 16 + g * (4 * TN);
@@ -655,38 +688,45 @@ uint64_t tiles(const GemmArgs& a, uint32_t bm, uint32_t bn) {
   return (uint64_t)((a.batch + bm - 1) / bm) * ((a.rows + bn - 1) / bn);
 }
 
-template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, int AHEAD = 0>
+template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, bool LOOSE = false, int KG = 1>
 ecw_status launch_tile(hipStream_t stream, const GemmArgs& a, int y_dtype) {
-  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY, AHEAD>;
+  using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY, LOOSE, KG>;
   const uint32_t m_tiles = (a.batch + T::BM - 1) / T::BM, n_tiles = (a.rows + T::BN - 1) / T::BN;
   if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
-  hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS, EARLY, AHEAD>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves), 0,
+  hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS, EARLY, LOOSE, KG>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves * KG), 0,
                      stream, a, m_tiles, n_tiles, y_dtype);
   return launched("mx4_gemm");
 }
 
-// Tiles by size: the smallest that leaves no CU two of them, for spans are waited for and
-// small ones wait least; when there are more, the largest, which reads least.  Measured
-// with bf16 x, in us (64x64, 64x128, 128x128, 128x256): 64 rows by 4096 x 14336 60.5, 67.7,
-// 104, 161; 1024 by 4096 x 4096 -, 49.9, 38.7, 54.4; 512 by 14336 x 4096 -, 93, 75, 63.
+// Tiles by size: the smallest that leaves no CU two of them, for most of a small one's time
+// is waiting; when there are more, the largest, which reads least.  Measured with bf16 x,
+// in us (32x64, 64x64, 64x128, 128x128, 128x256):
+//   64 rows by 4096 x 14336    23.9  41.8  55.5   106   164
+//   128 rows by 14336 x 4096   37.0  32.6  22.6  35.6  52.0
+//   1024 rows by 4096 x 4096   67.4  62.2  47.3  39.2  54.9
+//   512 rows by 14336 x 4096    122   111  83.3  75.8  60.9
+// and with 4-bit x (64x64, 128x128, 128x256, 256x256):
+//   64 rows by 4096 x 14336    21.0  37.9  65.4   103
+//   256 rows by 14336 x 4096   31.8  18.3  25.0  36.9
+//   1024 rows by 14336 x 4096   105  63.1  55.3  44.1
 template <int ACT>
 ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   constexpr uint64_t kCus = 256;
   // A few rows go a block per 16 rows of w, which reads x once for each: more rows and a
-  // short K are better off in tiles (16 rows by 14336 x 4096 22.6 and 13.8 us, 4 rows 14.5;
-  // by 4096 x 14336 21.8 and 37.8).
+  // short K are better off in tiles (16 rows by 14336 x 4096 22.6 and 10.6 us, 4 rows 13.3;
+  // by 4096 x 14336 19.3 and 23.8).
   // Operands that start between two words are slow to load (16 rows by 4096 x 14335 54 us,
-  // in tiles 42; 4 rows 21).
+  // in tiles 35; 4 rows 20).
   const bool words = ACT == kActMX4 || (aligned(a.x, 4) && a.x_stride % 2 == 0);
   const bool few = a.batch <= 4 || (a.batch <= 16 && words && (tiles(a, 32, 64) < kCus / 2 || a.blocks > 4 * 48));
   if constexpr (ACT == kActMX4) {
     if (few) return launch_few<ACT, true>(stream, a, y_dtype);
-    if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 5, true>(stream, a, y_dtype);
-    if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 6, true>(stream, a, y_dtype);
+    if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 3, true, false, 4>(stream, a, y_dtype);
+    if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 3, true, false, 2>(stream, a, y_dtype);
     if (tiles(a, 128, 256) <= kCus) return launch_tile<ACT, 2, 4, 4, 4, 4, true>(stream, a, y_dtype);
     return launch_tile<ACT, 2, 4, 8, 4, 3, false>(stream, a, y_dtype);
   } else {
-    if (a.cols < 8) {
+    if (a.cols <= 8) {
       const uint64_t grid = ((uint64_t)a.batch * a.rows + 255) / 256;
       if (grid >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
       hipLaunchKernelGGL(k_mx4_gemm_narrow<ACT>, dim3((uint32_t)grid), dim3(256), 0, stream, a, y_dtype);
@@ -697,17 +737,17 @@ ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
       return near ? launch_few<ACT, true>(stream, a, y_dtype) : launch_few<ACT, false>(stream, a, y_dtype);
     }
     if (aligned(a.x, 16) && a.x_stride % 8 == 0 && a.cols % 8 == 0) {
-      if (a.batch <= 32) return launch_tile<ACT, 1, 4, 2, 1, 5, true>(stream, a, y_dtype);
-      if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 4, true>(stream, a, y_dtype);
-      if (tiles(a, 64, 128) <= kCus) return launch_tile<ACT, 2, 4, 2, 2, 5, true>(stream, a, y_dtype);
+      if (tiles(a, 32, 64) <= kCus) return launch_tile<ACT, 1, 4, 2, 1, 3, false, false, 4>(stream, a, y_dtype);
+      if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 3, true, false, 2>(stream, a, y_dtype);
+      if (tiles(a, 64, 128) <= kCus) return launch_tile<ACT, 2, 4, 2, 2, 3, false, false, 2>(stream, a, y_dtype);
       if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 3, false>(stream, a, y_dtype);
       return launch_tile<ACT, 2, 4, 4, 4, 3, false>(stream, a, y_dtype);
     }
-    if (a.batch <= 32) return launch_tile<ACT, 1, 4, 2, 1, 5, true, 4>(stream, a, y_dtype);
-    if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 4, true, 4>(stream, a, y_dtype);
-    if (tiles(a, 64, 128) <= kCus) return launch_tile<ACT, 2, 4, 2, 2, 5, true, 4>(stream, a, y_dtype);
-    if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 3, false, 3>(stream, a, y_dtype);
-    return launch_tile<ACT, 2, 4, 4, 4, 3, false, 2>(stream, a, y_dtype);
+    if (tiles(a, 32, 64) <= kCus) return launch_tile<ACT, 1, 4, 2, 1, 3, false, true, 4>(stream, a, y_dtype);
+    if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 3, false, true, 2>(stream, a, y_dtype);
+    if (tiles(a, 64, 128) <= kCus) return launch_tile<ACT, 2, 4, 2, 2, 3, false, true, 2>(stream, a, y_dtype);
+    if (tiles(a, 128, 128) <= kCus) return launch_tile<ACT, 2, 4, 4, 2, 3, false, true>(stream, a, y_dtype);
+    return launch_tile<ACT, 2, 4, 4, 4, 3, false, true>(stream, a, y_dtype);
   }
 }
 
