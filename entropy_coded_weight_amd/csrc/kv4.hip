@@ -487,7 +487,7 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, f32x4 o, float
 }
 
 // Blocks of four waves that a CU's registers hold.
-constexpr int at_once(int dim, int nq) { return nq == 1 ? (dim == 64 ? 4 : dim == 128 ? 3 : 2) : dim < 256 ? 2 : 1; }
+constexpr int at_once(int dim, int nq) { return nq == 2 || dim == 256 ? 2 : dim == 128 ? 3 : 4; }
 
 // A row's output: element 4 d + r of the lane (o[n][d][r]) is dimension 2 NB (4 g + r) + d.
 template <int NB, int NQ, bool F16>
@@ -645,38 +645,64 @@ __global__ void __launch_bounds__(256, at_once(32 * NB, NQ)) k_kv4_attend(Attend
   }
 }
 
-// The splits of a row joined, in their order: a wave per row, lane s first holding split
-// s's factor, then D / 64 dimensions.
-constexpr uint32_t kMostSplits = 64;
-template <int D, bool F16>
-__global__ void __launch_bounds__(256) k_kv4_join(const float* __restrict__ part, void* __restrict__ out, uint64_t all,
-                                                  uint32_t splits) {
+// The splits of a row joined: `per` waves for a row, each the splits of its turn, and
+// their sums in the order of the waves.  Lane s of every wave first holds the factors of
+// splits s, s + 64, ..., EACH of them, then D / 64 dimensions.  One sequence of 131072
+// tokens and 8 heads: 42 us, with at most 64 splits and a wave per row 62.
+constexpr uint32_t kMostSplits = 256, kJoinWaves = 16;
+template <int D, bool F16, int EACH>
+__global__ void __launch_bounds__(64 * kJoinWaves) k_kv4_join(const float* __restrict__ part, void* __restrict__ out,
+                                                              uint64_t all, uint32_t splits, uint32_t per) {
   constexpr int N = D / 64;
-  const uint32_t lane = threadIdx.x & 63;
-  const uint64_t at = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= all) return;
+  __shared__ float sums[kJoinWaves][D];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = wave % per;
+  const uint64_t mine = (uint64_t)blockIdx.x * ((blockDim.x >> 6) / per) + wave / per;
+  const uint64_t at = mine < all ? mine : all - 1;
   const float* cl = part + splits * all * D + at * 2;
-  const f32x2 mine = lane < splits ? *reinterpret_cast<const f32x2*>(cl + lane * all * 2) : f32x2{0.f, kNothing};
-  const bool some = has_weight(mine[1]);
-  float c = some ? mine[0] : -INFINITY;
+  f32x2 state[EACH];
+  float c = -INFINITY, l = 0.f, f[EACH];
+  bool seen = false;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const uint32_t s = lane + 64 * k;
+    state[k] = s < splits ? *reinterpret_cast<const f32x2*>(cl + s * all * 2) : f32x2{0.f, kNothing};
+    if (has_weight(state[k][1])) c = fmaxf(c, state[k][0]);
+  }
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) c = fmaxf(c, __shfl_xor(c, i));
-  const float f = some ? __builtin_amdgcn_exp2f(mine[0] - c) : 0.f;
-  float l = some ? f * mine[1] : 0.f;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const bool some = has_weight(state[k][1]);
+    f[k] = some ? __builtin_amdgcn_exp2f(state[k][0] - c) : 0.f;
+    l += some ? f[k] * state[k][1] : 0.f;
+    seen = seen || __any(state[k][1] != kNothing);
+  }
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) l += __shfl_xor(l, i);
-  const bool seen = __any(mine[1] != kNothing);
   float o[N] = {};
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
 #pragma unroll 8
-  for (uint32_t s = 0; s < splits; ++s) {
-    const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
-    const float* p = part + (s * all + at) * D + lane * N;
-    float x[N];
+    for (uint32_t s = 64 * k + first; s < min(splits, 64u * k + 64); s += per) {
+      const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f[k]), s % 64));
+      const float* p = part + (s * all + at) * D + lane * N;
+      float x[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = p[i];
+      for (int i = 0; i < N; ++i) x[i] = p[i];
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fs != 0.f ? fmaf(fs, x[i], o[i]) : o[i];  // a part of no weight may be unwritten
+      for (int i = 0; i < N; ++i) o[i] = fs != 0.f ? fmaf(fs, x[i], o[i]) : o[i];  // a part of no weight may be unwritten
+    }
   }
+  if (per > 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[wave][lane * N + i] = o[i];
+    __syncthreads();
+    if (first != 0) return;
+    for (uint32_t k = 1; k < per; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] += sums[wave + k][lane * N + i];
+  }
+  if (mine >= all) return;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float y = seen ? o[i] / l : 0.f;
@@ -748,7 +774,10 @@ Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* a
   const uint64_t group = at->q_heads / c->kv_heads;
   const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;
   const uint64_t rows = each * group;
-  p.nq = rows <= 16 ? 1 : 2;  // four take all registers: 275 us for 512 rows behind 16384 tokens, two 216
+  // Tiles of 16 rows a wave, 1 or 2.  Four take all registers: 275 us for 512 rows behind
+  // 16384 tokens, two 216.  So do two of dimension 256: 92 us for 300 rows of 6 heads
+  // behind 16000 tokens, one 81.
+  p.nq = rows <= 16 || c->head_dim == 256 ? 1 : 2;
   uint64_t tiles_q = (rows + 16 * p.nq - 1) / (16 * p.nq);
   const uint64_t most = 65535 / c->kv_heads;
   p.q_tiles = (uint32_t)(tiles_q < most ? tiles_q : most);
@@ -796,15 +825,21 @@ void launch_attend(hipStream_t stream, const AttendArgs& a) {
 
 template <int NB, bool F16>
 ecw_status launch_all(hipStream_t stream, const AttendArgs& a, const Plan& p) {
-  if (p.nq == 1)
+  if constexpr (NB == 8)
+    launch_attend<NB, 1, F16>(stream, a);
+  else if (p.nq == 1)
     launch_attend<NB, 1, F16>(stream, a);
   else
     launch_attend<NB, 2, F16>(stream, a);
   if (ecw_status s = launched("kv4_attend")) return s;
   if (a.splits == 1) return ECW_OK;
-  const uint64_t all = (uint64_t)a.t.rows * a.q_heads, grid = (all + 3) / 4;
-  hipLaunchKernelGGL((k_kv4_join<32 * NB, F16>), dim3((uint32_t)grid), dim3(256), 0, stream, a.part, a.o, all,
-                     a.splits);
+  const uint64_t all = (uint64_t)a.t.rows * a.q_heads;
+  uint32_t per = 1;  // up to 4 splits a wave, while there are few rows (8: a window of 4096 15.7 us, 4: 14.8)
+  while (per < kJoinWaves && a.splits > 4 * per && all * per < 4096) per *= 2;
+  const uint32_t waves = per < 4 ? 4 : per;
+  const uint64_t grid = (all * per + waves - 1) / waves;
+  auto* fn = a.splits <= 64 ? k_kv4_join<32 * NB, F16, 1> : k_kv4_join<32 * NB, F16, kMostSplits / 64>;
+  hipLaunchKernelGGL(fn, dim3((uint32_t)grid), dim3(64 * waves), 0, stream, a.part, a.o, all, a.splits, per);
   return launched("kv4_attend");
 }
 

@@ -179,6 +179,16 @@ def test_long_sequences_are_split_and_joined(dim, n):
     bed.check(bed.cache.attend(q, bed.table, I32(bed.lens), window=1000, sinks=9), q, [n, n], 1000, 9)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,rows", [([36000], 1), ([36000], 20), ([20000, 40], 2), ([0, 9000], 1), ([3000], 3)])
+def test_one_long_sequence(dim, lens, rows):
+    """As many splits as there are, and their number on both sides of 64 and of a wave's share."""
+    _say("attend long", dim, lens, rows)
+    bed = Bed(lens, 1, dim)
+    q = _normal(83, rows * len(lens), 2, dim)
+    bed.check(bed.cache.attend(q, bed.table, I32(lens)), q, [rows] * len(lens))
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("dim,group,rows", [(64, 8, [23, 1, 70, 0, 300]), (128, 4, [500, 3, 49, 1, 200]),
                                             (128, 1, [700, 600, 190, 1, 255]), (64, 1, [256, 257, 31, 33, 512])])
