@@ -9,6 +9,7 @@
 //   key scales   [P][NB]
 //   value scales [P / 4][NB][4]
 // Writing a token touches only bytes of its own, so appends never read.
+#include <algorithm>
 #include <type_traits>
 
 #include "mx4_common.h"
@@ -767,37 +768,53 @@ constexpr uint64_t kChunk = 12;  // tiles of 32 tokens of a split at least, for 
 // sequence's tokens.
 struct Plan {
   uint32_t nq, q_tiles, splits, chunk;
+  double time;  // estimate, in a tile of keys by one tile of rows with every wave of a CU at work
 };
 
-Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
+// The plan with nq tiles of 16 rows a wave, for sequences of `rows` rows and `tiles` tiles.
+Plan plan_with(uint32_t nq, uint64_t rows, uint64_t tiles, const ecw_kv4* c, uint32_t batch) {
   Plan p;
-  const uint64_t group = at->q_heads / c->kv_heads;
-  const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;
-  const uint64_t rows = each * group;
-  // Tiles of 16 rows a wave, 1 or 2.  Four take all registers: 275 us for 512 rows behind
-  // 16384 tokens, two 216.  So do two of dimension 256: 92 us for 300 rows of 6 heads
-  // behind 16000 tokens, one 81.
-  p.nq = rows <= 16 || c->head_dim == 256 ? 1 : 2;
-  uint64_t tiles_q = (rows + 16 * p.nq - 1) / (16 * p.nq);
-  const uint64_t most = 65535 / c->kv_heads;
+  p.nq = nq;
+  const uint64_t tiles_q = (rows + 16 * nq - 1) / (16 * nq), most = 65535 / c->kv_heads;
   p.q_tiles = (uint32_t)(tiles_q < most ? tiles_q : most);
-  uint64_t len = (uint64_t)r->table_width * c->page_tokens;
-  if (at->max_len && at->max_len < len) len = at->max_len;
-  if (at->window) {
-    const uint64_t seen = (uint64_t)at->window + at->sinks + each;
-    if (seen < len) len = seen;
-  }
-  const uint64_t tiles = (len + 31) / 32 + 1, blocks = (uint64_t)p.q_tiles * c->kv_heads * r->batch;
+  const uint64_t blocks = (uint64_t)p.q_tiles * c->kv_heads * batch, room = 256 * at_once((int)c->head_dim, (int)nq);
   // as many blocks as the card holds at once, and no second round of them: 32 sequences of
   // up to 32768 tokens take 209 us at 3 splits of each, 233 at 4
-  uint64_t splits = 256 * at_once((int)c->head_dim, (int)p.nq) / blocks;
+  uint64_t splits = room / blocks;
   const uint64_t top = (tiles + kChunk - 1) / kChunk;
   if (splits > top) splits = top;
   if (splits > kMostSplits) splits = kMostSplits;
   if (splits < 1) splits = 1;
   p.chunk = (uint32_t)((tiles + splits - 1) / splits);
   p.splits = (uint32_t)((tiles + p.chunk - 1) / p.chunk);
+  // a wave's tiles of keys, one after the other: each takes its latency, or its turn among
+  // those of the CU's other blocks
+  const double per_cu = (double)((blocks * p.splits + 255) / 256);
+  p.time = ((p.chunk + 3) / 4) * (nq == 2 ? std::max(3.2, 1.6 * per_cu) : std::max(2.5, per_cu));
   return p;
+}
+
+// One or two tiles of rows a wave: two take 1.6 times as long for a tile of keys, and half
+// the blocks (512 rows of 32 heads behind 16384 tokens 220 us, one 283; 20 rows of 256 heads
+// of sequences over 16000 tokens 158 and 189), but fewer blocks may leave CUs idle (615 rows
+// of dimension 64 over 3211 tokens, 16 sequences: 41 and 33 us; 48 rows over 8000 tokens, 64
+// heads of sequences: 48 and 40; 20 rows over 2935 tokens, 6 of them: 13.0 and 10.7).  Four take all registers
+// (512 rows behind 16384 tokens 275 and 216 us), and so do two of dimension 256 (300 rows of
+// 6 heads behind 16000 tokens 92 us, one 81).
+Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
+  const uint64_t group = at->q_heads / c->kv_heads;
+  const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;
+  uint64_t len = (uint64_t)r->table_width * c->page_tokens;
+  if (at->max_len && at->max_len < len) len = at->max_len;
+  if (at->window) {
+    const uint64_t seen = (uint64_t)at->window + at->sinks + each;
+    if (seen < len) len = seen;
+  }
+  const uint64_t rows = each * group, tiles = (len + 31) / 32 + 1;
+  const Plan one = plan_with(1, rows, tiles, c, r->batch);
+  if (rows <= 16 || c->head_dim == 256) return one;
+  const Plan two = plan_with(2, rows, tiles, c, r->batch);
+  return one.time < two.time ? one : two;
 }
 
 ecw_status check_attention(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
