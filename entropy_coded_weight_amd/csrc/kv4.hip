@@ -91,17 +91,25 @@ __device__ __forceinline__ uint32_t quantise_row(const void* x, int64_t at, uint
     return quantise_oct<DT == ECW_DT_F16>(load_oct16(static_cast<const uint16_t*>(x) + at, u * 8, dim), byte);
 }
 
-// A lane per 8 dimensions of one head of one row, keys and values both.  Bound by
-// memory; for a few rows by the latency of the page look-up and the loads behind it.
+// A block has 256 / octs neighbouring rows of one head: four tokens' values share lines,
+// which blocks on different dies would each write a part of.  Gives the lane's row and head.
+__device__ __forceinline__ uint32_t row_of(const Cache& c, uint32_t octs, uint32_t* head) {
+  const uint32_t group = blockIdx.x / c.heads;
+  *head = blockIdx.x - group * c.heads;
+  return group * (256 / octs) + threadIdx.x / octs;
+}
+
+// A lane per 8 dimensions of one head of one row, keys and values both.  Bound by memory
+// (16384 rows of 8 heads of 128 dimensions 19.7 us, 4.3 TB/s; 24.0 with a block's rows of
+// several heads); for a few rows by the latency of the page look-up and the loads next to
+// it (64 rows 3.6 us).
 template <int DT>
 __global__ void __launch_bounds__(256) k_kv4_append(Cache c, Batch t, const void* __restrict__ k,
                                                     const void* __restrict__ v, int64_t k_row, int64_t k_head,
                                                     int64_t v_row, int64_t v_head) {
-  const uint32_t octs = c.dim / 8, nb = c.dim / 32;
-  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  const uint32_t u = (uint32_t)(id % octs);
-  const uint64_t rh = id / octs;
-  const uint32_t row = (uint32_t)(rh / c.heads), head = (uint32_t)(rh - (uint64_t)row * c.heads);
+  const uint32_t octs = c.dim / 8, nb = c.dim / 32, u = threadIdx.x % octs;
+  uint32_t head;
+  const uint32_t row = row_of(c, octs, &head);
   if (row >= t.rows) return;  // whole blocks: a head's lanes stay together
   uint32_t kb, vb, at = 0;
   const uint32_t kc = quantise_row<DT>(k, row * k_row + head * k_head, u, c.dim, &kb);
@@ -123,14 +131,13 @@ __global__ void __launch_bounds__(256) k_kv4_append(Cache c, Batch t, const void
   }
 }
 
-// The values that append's rows stand for, [rows][heads][dim]; zeros where a row has no page.
+// The values that append's rows stand for, [rows][heads][dim]; zeros where a row has no
+// page.  Bound by memory (16384 rows of 8 heads of 128 dimensions 16.2 us, 5.2 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __restrict__ k, void* __restrict__ v) {
-  const uint32_t octs = c.dim / 8, nb = c.dim / 32;
-  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  const uint32_t u = (uint32_t)(id % octs);
-  const uint64_t rh = id / octs;
-  const uint32_t row = (uint32_t)(rh / c.heads), head = (uint32_t)(rh - (uint64_t)row * c.heads);
+  const uint32_t octs = c.dim / 8, nb = c.dim / 32, u = threadIdx.x % octs;
+  uint32_t head;
+  const uint32_t row = row_of(c, octs, &head);
   if (row >= t.rows) return;
   uint32_t at = 0, kc = 0, vc = 0, kb = kScaleOne, vb = kScaleOne;
   const uint8_t* from = place(c, t, row, head, &at);
@@ -146,8 +153,9 @@ __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __rest
     kb = s[at * nb + u / 4];
     vb = s[scale_bytes(c) + (at / 4 * nb + u / 4) * 4 + at % 4];
   }
-  store_oct<DT>(k, id * 8, kc, scale_of(kb), 8);
-  store_oct<DT>(v, id * 8, vc, scale_of(vb), 8);
+  const uint64_t to = (((uint64_t)row * c.heads + head) * octs + u) * 8;
+  store_oct<DT>(k, to, kc, scale_of(kb), 8);
+  store_oct<DT>(v, to, vc, scale_of(vb), 8);
 }
 
 // ------------------------------------------------------------------ attention
@@ -164,6 +172,15 @@ __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __rest
 // With a bf16 query keys, values and weights are bf16; with an fp16 query fp16, which
 // holds keys and values exactly between scales of 2^-23 and 2^13, all that fp16 keys and
 // values can have.  Smaller ones round to multiples of 2^-24, larger ones count as NaN.
+//
+// Four waves of a block take tiles of 32 tokens in turn, straight into registers, the next
+// one asked for while one is multiplied.  For single tokens bound by memory (32 sequences
+// up to 32768 tokens, 8 heads of 128 dimensions: 195 us, 4.4 TB/s of cache), for short ones
+// by the latency of lengths, page table and pages in turn (1001 tokens 7.7 us, and 3.5 for
+// the join), for many rows by vector instructions, which unpack 4-bit values and take
+// exponentials (512 rows of 32 heads behind 16384 tokens 231 us, 590 TFLOP/s).  Blocks whose
+// waves share a tile's operands through LDS took 257 us there: the copies, one tile ahead,
+// were waited for.
 struct AttendArgs {
   Cache c;
   Batch t;
@@ -757,7 +774,8 @@ Batch batch_of(const ecw_kv4_rows* r) {
 }
 
 bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
-  const uint64_t n = ((uint64_t)r->rows * c->kv_heads * (c->head_dim / 8) + 255) / 256;
+  const uint32_t rows = 256 / (c->head_dim / 8);
+  const uint64_t n = ((uint64_t)r->rows + rows - 1) / rows * c->kv_heads;
   *grid = (uint32_t)n;
   return n >> 31 == 0;
 }
@@ -796,11 +814,11 @@ Plan plan_with(uint32_t nq, uint64_t rows, uint64_t tiles, const ecw_kv4* c, uin
 
 // One or two tiles of rows a wave: two take 1.6 times as long for a tile of keys, and half
 // the blocks (512 rows of 32 heads behind 16384 tokens 220 us, one 283; 20 rows of 256 heads
-// of sequences over 16000 tokens 158 and 189), but fewer blocks may leave CUs idle (615 rows
-// of dimension 64 over 3211 tokens, 16 sequences: 41 and 33 us; 48 rows over 8000 tokens, 64
-// heads of sequences: 48 and 40; 20 rows over 2935 tokens, 6 of them: 13.0 and 10.7).  Four take all registers
-// (512 rows behind 16384 tokens 275 and 216 us), and so do two of dimension 256 (300 rows of
-// 6 heads behind 16000 tokens 92 us, one 81).
+// of sequences over 16000 tokens 158 and 189), but fewer blocks may leave CUs idle (615
+// rows of dimension 64 over 3211 tokens, 16 sequences: 41 and 33 us; 48 rows over 8000
+// tokens, 64 heads of sequences: 48 and 40; 20 rows over 2935 tokens, 6 of them: 13.0 and
+// 10.7).  Four take all registers (512 rows behind 16384 tokens 275 and 216 us), and so do
+// two of dimension 256 (300 rows of 6 heads behind 16000 tokens 92 us, one 81).
 Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
   const uint64_t group = at->q_heads / c->kv_heads;
   const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;
