@@ -799,7 +799,11 @@ Plan plan_with(uint32_t nq, uint64_t rows, uint64_t tiles, const ecw_kv4* c, uin
   // as many blocks as the card holds at once, and no second round of them: 32 sequences of
   // up to 32768 tokens take 209 us at 3 splits of each, 233 at 4
   uint64_t splits = room / blocks;
-  const uint64_t top = (tiles + kChunk - 1) / kChunk;
+  uint64_t top = (tiles + kChunk - 1) / kChunk;
+  // a tile a wave where CUs are idle and a join is needed anyway (1001 tokens of 8 heads
+  // 10.6 -> 9.0 us; 300 tokens, one split, 7.5 us and 8.7 in three; a window of 4096 of 64
+  // heads of sequences in splits of 12 tiles 14.8 us, of 8 15.4)
+  if (top > 1) top = std::max(top, std::min<uint64_t>({(tiles + 3) / 4, 16, 512 / blocks}));
   if (splits > top) splits = top;
   if (splits > kMostSplits) splits = kMostSplits;
   if (splits < 1) splits = 1;
