@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __rest
 // Four waves of a block take tiles of 32 tokens in turn, straight into registers, the next
 // one asked for while one is multiplied.  For single tokens bound by memory (32 sequences
 // up to 32768 tokens, 8 heads of 128 dimensions: 195 us, 4.4 TB/s of cache), for short ones
-// by the latency of lengths, page table and pages in turn (1001 tokens 7.7 us, and 3.5 for
+// by the latency of lengths, page table and pages in turn (1001 tokens 5.5 us, and 3.9 for
 // the join), for many rows by vector instructions, which unpack 4-bit values and take
 // exponentials (512 rows of 32 heads behind 16384 tokens 231 us, 590 TFLOP/s).  Blocks whose
 // waves share a tile's operands through LDS took 257 us there: the copies, one tile ahead,
