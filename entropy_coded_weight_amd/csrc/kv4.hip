@@ -341,6 +341,12 @@ struct Wave {
     t.vs[h] = (t.vs[h] & ~(255u << 8 * i)) | kScaleOne << 8 * i;
   }
 
+  // Past fp16's range some of a block's keys would become infinities, and a token with a score
+  // of -infinity would vanish without a sign: the whole block counts as NaN.
+  static __device__ __forceinline__ float key_scale(uint32_t byte) {
+    return scale_of(F16 && byte > kScaleOne + 13 ? kScaleNaN : byte);
+  }
+
   __device__ __forceinline__ void scores(const Tile<NB>& t, f32x4 (&s)[2][NQ]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -348,7 +354,7 @@ struct Wave {
       for (int n = 0; n < NQ; ++n) s[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        const u32x4 k = oct<F16>(t.k[h][j], scale_of(t.ks[h] >> 8 * (j / 4) & 255));
+        const u32x4 k = oct<F16>(t.k[h][j], key_scale(t.ks[h] >> 8 * (j / 4) & 255));
 #pragma unroll
         for (int n = 0; n < NQ; ++n) s[h][n] = mfma16<F16>(k, q[n][j], s[h][n]);
       }

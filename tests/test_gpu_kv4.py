@@ -439,3 +439,23 @@ def test_refusals():
     for args in ((1, 1, 96), (1, 1, 64, 48)):
         with pytest.raises(ecw.EcwError):
             ecw.KV4Cache(*args)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("value", [1e6, -1e6, 65536.0])
+def test_fp16_queries_over_keys_past_their_range(value, dim, n):
+    """A key block past fp16's range is NaN to the rows that see it, whatever the sign and
+    size of its product with the query, and nothing to the others; 65504 is in the range."""
+    _say("attend fp16 key range", value, dim, n)
+    k, v = [_normal(1, 200, 1, dim)], [_normal(2, 200, 1, dim)]
+    k[0][190, 0, 3] = value
+    k[0][195, 0, dim - 1] = 49152.0  # the largest that fp16 holds in 4 bits
+    bed = Bed([200], 1, dim, k=k, v=v)
+    bed.k[0] = k[0].clone()
+    bed.k[0][190, 0, :32] = float("nan")
+    q = _normal(92, n, 2, dim, dtype=FP16)
+    q[:, :, 3] = 1e-4
+    q[:, :, dim - 1] = 1e-4
+    bed.check(bed.cache.attend(q, bed.table, I32([200])), q, [n])
+    bed.check(bed.cache.attend(q, bed.table, I32([200]), window=6), q, [n], 6)
