@@ -205,10 +205,6 @@ __device__ __forceinline__ void store_oct(void* out, uint64_t at, uint32_t codes
   }
 }
 
-__device__ __forceinline__ bool has_nan_scale(uint32_t w) {  // a byte of 255
-  return (((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u) != 0;
-}
-
 // blocks of a row, padded to whole 128-column spans: what a wave takes at a time
 inline __host__ __device__ uint32_t row_blocks(uint32_t cols) { return (cols + 127) / 128 * 4; }
 // bytes from one row's scales to the next: 16 bytes, the scales of four spans, are read at once

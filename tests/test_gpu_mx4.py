@@ -350,3 +350,38 @@ def test_gemm_narrow_rows(cols, dtype, out):
     assert y[:, 7].isnan().all()
     w, y = torch.cat([w[:7], w[8:]]), torch.cat([y[:, :7], y[:, 8:]], 1)
     _check_product(w, x, y)
+
+
+@pytest.mark.parametrize("batch", [2, 12, 40, 140])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_gemm_infinite_x_next_to_scales_far_apart(batch, dtype):
+    """An infinity in x gives the definition's infinity or NaN in every output, whatever the
+    neighbouring rows of w hold: close scales, far ones, a NaN block."""
+    _say("gemm inf, far scales", batch, dtype)
+    w = _matrix(70, 512, torch.float32, seed=7, spread=0)
+    w[3, 64:96] *= 2.0 ** -40    # rows 0..15 next to a row of far scales
+    w[20, 100] = float("nan")    # rows 16..31 next to a NaN block
+    w.view(70, 16, 32)[40, ::2] *= 2.0 ** -30
+    w[50:52] = 0                 # zeros times an infinity
+    x = _matrix(batch, 512, dtype, seed=8, spread=0)
+    x[0, 70], x[1, 5], x[1, 300] = float("inf"), -float("inf"), -float("inf")
+    y = F64(ecw.mx4_quantize(w).gemm(x))
+    with np.errstate(invalid="ignore"):
+        want = F64(x) @ R.rounded(F64(w)).T
+    assert np.array_equal(np.isnan(y), np.isnan(want)), "NaN elsewhere"
+    inf = np.isinf(want)
+    assert inf.any() and np.array_equal(y[inf], want[inf])
+    keep = ~np.isin(np.arange(70), [20])
+    _check_product(w[keep], x[2:], torch.from_numpy(y[2:][:, keep]).float())
+
+
+@pytest.mark.parametrize("batch", [2, 40])
+def test_gemm_every_nan_is_nan_next_to_scales_far_apart(batch):
+    _say("gemm NaN payloads", batch)
+    w = _matrix(33, 256, torch.float32, seed=7, spread=0)
+    w[3, 64:96] *= 2.0 ** -40
+    x = _matrix(batch, 256, torch.float16, seed=8, spread=0)
+    for payload in (0x7c01, 0x7e00, 0x7fff, -0x3ff):  # signalling, quiet, all ones, negative
+        x[1, 70].view(torch.int16).fill_(payload)
+        y = ecw.mx4_quantize(w).gemm(x)
+        assert bool(torch.isnan(y[1]).all()) and bool(torch.isfinite(y[0]).all())
