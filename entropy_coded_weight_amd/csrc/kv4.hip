@@ -672,7 +672,9 @@ __global__ void __launch_bounds__(256, at_once(32 * NB, NQ)) k_kv4_attend(Attend
 // The splits of a row joined: `per` waves for a row, each the splits of its turn, and
 // their sums in the order of the waves.  Lane s of every wave first holds the factors of
 // splits s, s + 64, ..., EACH of them, then D / 64 dimensions.  One sequence of 131072
-// tokens and 8 heads: 42 us, with at most 64 splits and a wave per row 62.
+// tokens and 8 heads: 42 us, with at most 64 splits and a wave per row 62.  A split in which
+// the row saw nothing may be unwritten and is passed over; one whose weight is zero counts,
+// for it may hold a NaN.
 constexpr uint32_t kMostSplits = 256, kJoinWaves = 16;
 template <int D, bool F16, int EACH>
 __global__ void __launch_bounds__(64 * kJoinWaves) k_kv4_join(const float* __restrict__ part, void* __restrict__ out,
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) k_kv4_join(const float* __res
 #pragma unroll
   for (int k = 0; k < EACH; ++k) {
     const bool some = has_weight(state[k][1]);
-    f[k] = some ? __builtin_amdgcn_exp2f(state[k][0] - c) : 0.f;
+    f[k] = some ? __builtin_amdgcn_exp2f(state[k][0] - c) : state[k][1] == kNothing ? kNothing : 0.f;
     l += some ? f[k] * state[k][1] : 0.f;
     seen = seen || __any(state[k][1] != kNothing);
   }
@@ -714,7 +716,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) k_kv4_join(const float* __res
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = p[i];
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = fs != 0.f ? fmaf(fs, x[i], o[i]) : o[i];  // a part of no weight may be unwritten
+      for (int i = 0; i < N; ++i) o[i] = fs != kNothing ? fmaf(fs, x[i], o[i]) : o[i];
     }
   }
   if (per > 1) {

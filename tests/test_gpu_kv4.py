@@ -459,3 +459,20 @@ def test_fp16_queries_over_keys_past_their_range(value, dim, n):
     q[:, :, dim - 1] = 1e-4
     bed.check(bed.cache.attend(q, bed.table, I32([200])), q, [n])
     bed.check(bed.cache.attend(q, bed.table, I32([200]), window=6), q, [n], 6)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("n", [1, 20])
+def test_a_visible_nan_value_of_no_weight_is_nan_in_every_split(n, dtype):
+    """A weight may be too small for any number, but 0 times NaN is NaN, in whichever split
+    of the tokens the value lies."""
+    _say("attend NaN of no weight", n, dtype)
+    k = [torch.full((5000, 1, 64), -6.0, dtype=BF16, device="cuda")]
+    v = [_normal(2, 5000, 1, 64)]
+    k[0][4000] = 6.0
+    v[0][5, 0, 40] = float("nan")
+    bed = Bed([5000], 1, 64, k=k, v=v)
+    q = torch.full((n, 2, 64), 8.0, dtype=dtype, device="cuda")  # scores of 384 and -384
+    for hints in ({}, {"max_len": 1}, {"max_len": 1000}, {"max_len": 5000}):
+        bed.check(bed.cache.attend(q, bed.table, I32([5000]), **hints), q, [n])
+    bed.check(bed.cache.attend(q, bed.table, I32([5000]), window=4000), q, [n], 4000)
