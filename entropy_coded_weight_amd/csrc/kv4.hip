@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __rest
 // 4 (l / 16) .. + 3 of each half tile, which is the operand of O^T += V^T P^T if that
 // instruction's order of tokens is taken the same way.  A third product, of ones, sums
 // the weights as they were rounded.  Weights are 2^(scale s - c) with an offset c of the
-// lane's own query column that only moves when a weight would pass 2^8, so that most
-// tiles need neither a maximum across lanes nor a rescaling.
+// lane's own query column that only moves when a weight would pass 2^8 times the one it was
+// set by, so that most tiles need neither a maximum across lanes nor a rescaling.
 //
 // With a bf16 query keys, values and weights are bf16; with an fp16 query fp16, which
 // holds keys and values exactly between scales of 2^-23 and 2^13, all that fp16 keys and
@@ -316,9 +316,11 @@ __device__ __forceinline__ void each(F&& f) {
 
 template <int NB, int NQ, bool F16>
 struct Wave {
-  // fp16 weights stand 2^7 higher than bf16's: fp16 ends at 2^15, and what is lost at its
-  // other end is then under 2^-31 of the largest weight
-  static constexpr float kTop = F16 ? 7.f : 0.f, kSlack = 8.f;
+  // Exponent of the largest weight when an offset is set.  fp16 ends at 2^15, and what is lost
+  // at its other end is then under 2^-31 of the largest weight.  bf16 values end at 2^128, as
+  // the fp32 sums do: weights far under one keep sums of 2^24 tokens from passing the end, and
+  // reach down to 2^-94 of the largest.
+  static constexpr float kTop = F16 ? 7.f : -32.f, kSlack = 8.f;
 
   u32x4 q[NQ][NB];
   int32_t pos[NQ];  // of the lane's query row in each tile, -1: no row

@@ -476,3 +476,19 @@ def test_a_visible_nan_value_of_no_weight_is_nan_in_every_split(n, dtype):
     for hints in ({}, {"max_len": 1}, {"max_len": 1000}, {"max_len": 5000}):
         bed.check(bed.cache.attend(q, bed.table, I32([5000]), **hints), q, [n])
     bed.check(bed.cache.attend(q, bed.table, I32([5000]), window=4000), q, [n], 4000)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 20])
+def test_values_near_the_end_of_the_range(dim, n):
+    """bf16 values up to 2^127: an average of them is one of them, not an infinity."""
+    _say("attend large values", dim, n)
+    lens = [300, 6000]
+    v = [torch.full((m, 1, dim), 2.0 ** 127, dtype=BF16, device="cuda") for m in lens]
+    bed = Bed(lens, 1, dim, v=v)
+    q = _normal(79, 2 * n, 2, dim, scale=2.0)
+    o = bed.cache.attend(q, bed.table, I32(lens))
+    bed.check(o, q, [n, n])
+    v = [_normal(3, m, 1, dim, scale=2.0 ** -70) for m in lens]  # and small ones keep their bits
+    bed = Bed(lens, 1, dim, v=v)
+    bed.check(bed.cache.attend(q, bed.table, I32(lens)), q, [n, n], grid=2.0 ** -100)
