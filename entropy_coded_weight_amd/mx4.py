@@ -53,10 +53,13 @@ def _native():
 
 def _on(stream, tensors, call):
     """call() with `stream` current; the tensors live on until its work is done."""
+    tensors = [t for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda]
+    for t in tensors:  # work goes to the tensors' device, whose current stream would be another one
+        if t.device != stream.device:
+            raise ValueError(f"the stream is on {stream.device}, an operand on {t.device}")
     with torch.cuda.stream(stream):
         for t in tensors:
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
+            t.record_stream(stream)
         return call()
 
 

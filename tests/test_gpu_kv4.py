@@ -8,6 +8,8 @@ rounding of 2^-23 of sum |q k| for each of the D / 32 instructions and the 64 ad
 inside, and 2^-18 for the exponential's argument and result (scores here stay under
 2^5, half an fp32 step of 2^-19 there).  The sums over tokens add 2^-23 for each of
 the T / 32 tiles and 128 more.  Then half a step of the output type."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -492,3 +494,18 @@ def test_values_near_the_end_of_the_range(dim, n):
     v = [_normal(3, m, 1, dim, scale=2.0 ** -70) for m in lens]  # and small ones keep their bits
     bed = Bed(lens, 1, dim, v=v)
     bed.check(bed.cache.attend(q, bed.table, I32(lens)), q, [n, n], grid=2.0 ** -100)
+
+
+def test_a_stream_of_another_device_is_refused():
+    other = SimpleNamespace(device=torch.device("cuda", 1))  # refused before anything is done with it
+    bed = Bed([40], 2, 64)
+    q, lens = _normal(1, 1, 4, 64), I32([40])
+    k = q[:, :2].contiguous()
+    w = ecw.mx4_quantize(_normal(2, 16, 64))
+    for call in (lambda: bed.cache.attend(q, bed.table, lens, stream=other),
+                 lambda: bed.cache.append(k, k, bed.table, lens, stream=other),
+                 lambda: bed.cache.read(bed.table, lens, 1, stream=other),
+                 lambda: ecw.mx4_quantize(q[0], stream=other), lambda: w.dequantize(stream=other),
+                 lambda: w.gemm(_normal(3, 2, 64), stream=other), lambda: w.gemm(w, stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
