@@ -88,6 +88,11 @@ int64_t whole(PyObject* o, const char* name, int64_t most) {
   return v;
 }
 
+// What a call writes advances its version, so that autograd notices if it holds the tensor.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // the given output, or a new one
 at::Tensor output(PyObject* o, const at::Tensor& like, at::IntArrayRef shape, at::ScalarType type, const char* name) {
   if (o == Py_None) return at::empty(shape, like.options().dtype(type));
@@ -97,6 +102,7 @@ at::Tensor output(PyObject* o, const at::Tensor& like, at::IntArrayRef shape, at
     for (int64_t v : shape) s += (s.empty() ? "" : ", ") + std::to_string(v);
     bad_value(std::string(name) + " must be a contiguous (" + s + ") tensor on " + like.device().str());
   }
+  written(t);
   return t;
 }
 
@@ -279,6 +285,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const ecw_kv4_rows r = rows_of(c, a[2], a[3], a[4], k.size(0));
     const int64_t strides[4] = {k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
     const c10::DeviceGuard guard(c.data.device());
+    written(c.data);
     check(api.append(stream_of(c.data.device()), &c.c, &r, k.data_ptr(), v.data_ptr(), dt, strides), "kv4_append");
     Py_RETURN_NONE;
   });
@@ -329,8 +336,8 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (PyErr_Occurred()) throw Raised{};
     }
     const c10::DeviceGuard guard(c.data.device());
+    if (a[9] != Py_None && tensor(a[9], "out").scalar_type() != q.scalar_type()) bad_value("out must have q's dtype");
     const at::Tensor out = output(a[9], q, {rows, q_heads, (int64_t)c.c.head_dim}, q.scalar_type(), "out");
-    if (out.scalar_type() != q.scalar_type()) bad_value("out must have q's dtype");
     size_t bytes = 0;
     check(api.workspace(&c.c, &r, &at, &bytes), "kv4_attend_workspace_size");
     at::Tensor ws;

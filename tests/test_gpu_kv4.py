@@ -509,3 +509,29 @@ def test_a_stream_of_another_device_is_refused():
                  lambda: w.gemm(_normal(3, 2, 64), stream=other), lambda: w.gemm(w, stream=other)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+def test_given_outputs_count_as_written():
+    """out= and y= advance the tensors' versions, so that autograd notices if it holds them."""
+    x = _normal(1, 4, 64)
+    w = ecw.mx4_quantize(x)
+    y, d = torch.empty(4, 4, device="cuda"), torch.empty(4, 64, device="cuda")
+    bed = Bed([40], 2, 64)
+    q, lens = _normal(1, 1, 4, 64), I32([40])
+    o = torch.empty_like(q)
+    for t, call in ((y, lambda: w.gemm(x, y=y)), (y, lambda: w.gemm(w, y=y)), (d, lambda: w.dequantize(out=d)),
+                    (w.codes, lambda: ecw.mx4_quantize(x, out=w)), (w.scales, lambda: ecw.mx4_quantize(x, out=w)),
+                    (o, lambda: bed.cache.attend(q, bed.table, lens, out=o)),
+                    (bed.cache.data, lambda: bed.cache.append(q[:, :2], q[:, 2:], bed.table, lens))):
+        before = t._version
+        call()
+        assert t._version > before
+    with torch.inference_mode():
+        inside = torch.empty(4, 4, device="cuda")
+    assert torch.equal(w.gemm(x, y=inside), w.gemm(x))  # has no version to advance
+    a = torch.ones(1, 4, 64, device="cuda", requires_grad=True)
+    held = torch.ones(1, 4, 64, dtype=BF16, device="cuda")
+    loss = (a * held).sum()
+    bed.cache.attend(q, bed.table, lens, out=held)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
