@@ -790,6 +790,7 @@ bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
   return n >> 31 == 0;
 }
 
+constexpr float kLog2E = 1.44269504088896f;
 constexpr uint64_t kChunk = 12;  // tiles of 32 tokens of a split at least, for its four waves
 
 // How an attention call is cut up: query tiles of 16 nq rows, and splits of each
@@ -858,7 +859,8 @@ ecw_status check_attention(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv
     return refuse(ECW_E_UNSUPPORTED, "rows times q_heads must be below 2^31");
   if (at->window > 1u << 30 || at->sinks > 1u << 30)
     return refuse(ECW_E_INVALID_ARG, "window and sinks must be at most 2^30");
-  if (!(at->scale - at->scale == 0.f)) return refuse(ECW_E_INVALID_ARG, "scale must be finite");
+  const float scale = at->scale * kLog2E;
+  if (!(scale - scale == 0.f)) return refuse(ECW_E_INVALID_ARG, "scale must be finite, times log2(e) too");
   return ECW_OK;
 }
 
@@ -988,7 +990,7 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
   a.per_page = page_tiles == 1 ? 0 : (uint32_t)(((uint64_t(1) << 32) + page_tiles - 1) / page_tiles);
   a.window = (int32_t)at->window;
   a.sinks = (int32_t)at->sinks;
-  a.scale = at->scale * 1.44269504088896f;
+  a.scale = at->scale * kLog2E;
   return dtype == ECW_DT_F16 ? launch_dim<true>((hipStream_t)stream, a, p)
                              : launch_dim<false>((hipStream_t)stream, a, p);
 }

@@ -420,7 +420,7 @@ typedef struct {
   uint32_t max_len;          /* most tokens of one sequence, 0 unknown: for the launch's shape only */
   uint32_t window;           /* a row sees its last `window` tokens, its own among them; 0: all */
   uint32_t sinks;            /* and, with a window, the first `sinks` tokens */
-  float scale;               /* of the scores */
+  float scale;               /* of the scores; it and scale * log2(e) finite */
 } ecw_kv4_attention;
 
 ecw_status kv4_bytes(const ecw_kv4* cache, size_t* bytes);

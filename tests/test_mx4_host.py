@@ -139,3 +139,10 @@ def test_tensors_off_the_gpu_are_refused():
         ecw.MX4Tensor(torch.zeros(2, 64, dtype=torch.uint8), torch.zeros(2, 4, dtype=torch.uint8), 2, 128)
     with pytest.raises(ValueError):
         ecw.KV4Cache(0, 1, 64)
+
+
+def test_scale_that_log2_e_takes_past_the_range(L):
+    """Scores are taken to base 2: scale * log2(e) has to be a number too."""
+    n = ctypes.c_size_t(0)
+    for scale, status in ((2.3e38, OK), (-2.3e38, OK), (2.5e38, INVALID), (-3.4e38, INVALID)):
+        assert L.kv4_attend_workspace_size(_cache({}), _rows({}), _attention({"scale": scale}), n) == status
