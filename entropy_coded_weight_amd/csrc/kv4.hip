@@ -787,7 +787,7 @@ bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
   const uint32_t rows = 256 / (c->head_dim / 8);
   const uint64_t n = ((uint64_t)r->rows + rows - 1) / rows * c->kv_heads;
   *grid = (uint32_t)n;
-  return n >> 31 == 0;
+  return launchable(n, 256);
 }
 
 constexpr float kLog2E = 1.44269504088896f;
@@ -801,7 +801,7 @@ struct Plan {
 };
 
 // The plan with nq tiles of 16 rows a wave, for sequences of `rows` rows and `tiles` tiles.
-Plan plan_with(uint32_t nq, uint64_t rows, uint64_t tiles, const ecw_kv4* c, uint32_t batch) {
+Plan plan_with(uint32_t nq, uint64_t rows, uint64_t tiles, const ecw_kv4* c, uint32_t batch, bool joinable) {
   Plan p;
   p.nq = nq;
   const uint64_t tiles_q = (rows + 16 * nq - 1) / (16 * nq), most = 65535 / c->kv_heads;
@@ -817,6 +817,7 @@ Plan plan_with(uint32_t nq, uint64_t rows, uint64_t tiles, const ecw_kv4* c, uin
   if (top > 1) top = std::max(top, std::min<uint64_t>({(tiles + 3) / 4, 16, 512 / blocks}));
   if (splits > top) splits = top;
   if (splits > kMostSplits) splits = kMostSplits;
+  if (!joinable) splits = 1;
   if (splits < 1) splits = 1;
   p.chunk = (uint32_t)((tiles + splits - 1) / splits);
   p.splits = (uint32_t)((tiles + p.chunk - 1) / p.chunk);
@@ -844,9 +845,10 @@ Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* a
     if (seen < len) len = seen;
   }
   const uint64_t rows = each * group, tiles = (len + 31) / 32 + 1;
-  const Plan one = plan_with(1, rows, tiles, c, r->batch);
+  const bool joinable = launchable((uint64_t)r->rows * at->q_heads + kJoinWaves, 64);  // a wave for each, at least
+  const Plan one = plan_with(1, rows, tiles, c, r->batch, joinable);
   if (rows <= 16 || c->head_dim == 256) return one;
-  const Plan two = plan_with(2, rows, tiles, c, r->batch);
+  const Plan two = plan_with(2, rows, tiles, c, r->batch, joinable);
   return one.time < two.time ? one : two;
 }
 

@@ -214,6 +214,9 @@ inline __host__ __device__ uint32_t scale_stride(uint32_t cols) { return (cols +
 ecw_status refuse(ecw_status s, const char* msg) noexcept;
 ecw_status launched(const char* what) noexcept;  // the status after a launch
 
+// A launch has fewer than 2^32 threads along its grid.
+inline bool launchable(uint64_t blocks, uint32_t threads) { return blocks * threads >> 32 == 0; }
+
 inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace ecw

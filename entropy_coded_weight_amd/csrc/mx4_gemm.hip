@@ -715,6 +715,7 @@ ecw_status launch_few(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   // up to four pairs a wave, and waves enough to fill the card
   uint32_t waves = 4;
   while (waves < kFewWaves && (pairs > waves * kTurns || ((uint64_t)nt * waves < 2048 && waves < pairs))) waves *= 2;
+  if (!launchable(nt, waves * 64)) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
   const uint32_t lds = waves * kTurns * kTurnBytes;
   auto* fn = k_mx4_gemm_few<ACT, NEAR>;
   if (lds > 64 * 1024) {  // to be allowed once on each device
@@ -742,7 +743,8 @@ template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, bool LOOS
 ecw_status launch_tile(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   using T = Tiles<ACT, WM, WN, TM, TN, NS, EARLY, LOOSE, KG>;
   const uint32_t m_tiles = (a.batch + T::BM - 1) / T::BM, n_tiles = (a.rows + T::BN - 1) / T::BN;
-  if ((uint64_t)m_tiles * n_tiles >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
+  if (!launchable((uint64_t)m_tiles * n_tiles, 64 * T::kWaves * KG))
+    return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
   hipLaunchKernelGGL((k_mx4_gemm_tile<ACT, WM, WN, TM, TN, NS, EARLY, LOOSE, KG>), dim3(m_tiles * n_tiles), dim3(64 * T::kWaves * KG), 0,
                      stream, a, m_tiles, n_tiles, y_dtype);
   return launched("mx4_gemm");
@@ -778,7 +780,7 @@ ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   } else {
     if (a.cols <= 8) {
       const uint64_t grid = ((uint64_t)a.batch * a.rows + 255) / 256;
-      if (grid >> 31) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
+      if (!launchable(grid, 256)) return refuse(ECW_E_UNSUPPORTED, "product too large for one launch");
       hipLaunchKernelGGL(k_mx4_gemm_narrow<ACT>, dim3((uint32_t)grid), dim3(256), 0, stream, a, y_dtype);
       return launched("mx4_gemm");
     }

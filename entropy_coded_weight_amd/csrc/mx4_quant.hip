@@ -90,7 +90,7 @@ ecw_status mx4_quantize(ecw_stream stream, const void* x, int x_dtype, int64_t r
   if (row_stride < 0) return refuse(ECW_E_INVALID_ARG, "row stride must not be negative");
   const uint32_t octs = row_blocks(cols) * 4;
   const uint64_t grid = ((uint64_t)rows * octs + 255) / 256;
-  if (grid >> 31) return refuse(ECW_E_UNSUPPORTED, "matrix too large for one launch");
+  if (!launchable(grid, 256)) return refuse(ECW_E_UNSUPPORTED, "matrix too large for one launch");
   auto* fn = x_dtype == ECW_DT_F32   ? k_mx4_quantise<ECW_DT_F32>
              : x_dtype == ECW_DT_F16 ? k_mx4_quantise<ECW_DT_F16>
                                      : k_mx4_quantise<ECW_DT_BF16>;
@@ -109,7 +109,7 @@ ecw_status mx4_dequantize(ecw_stream stream, const void* codes, const void* scal
   if (!out || !aligned(out, size)) return refuse(ECW_E_INVALID_ARG, "output must be an aligned device pointer");
   const uint32_t octs = row_blocks(cols) * 4;
   const uint64_t grid = ((uint64_t)rows * octs + 255) / 256;
-  if (grid >> 31) return refuse(ECW_E_UNSUPPORTED, "matrix too large for one launch");
+  if (!launchable(grid, 256)) return refuse(ECW_E_UNSUPPORTED, "matrix too large for one launch");
   auto* fn = out_dtype == ECW_DT_F32   ? k_mx4_dequantise<ECW_DT_F32>
              : out_dtype == ECW_DT_F16 ? k_mx4_dequantise<ECW_DT_F16>
                                        : k_mx4_dequantise<ECW_DT_BF16>;

@@ -146,3 +146,29 @@ def test_scale_that_log2_e_takes_past_the_range(L):
     n = ctypes.c_size_t(0)
     for scale, status in ((2.3e38, OK), (-2.3e38, OK), (2.5e38, INVALID), (-3.4e38, INVALID)):
         assert L.kv4_attend_workspace_size(_cache({}), _rows({}), _attention({"scale": scale}), n) == status
+
+
+def test_launches_past_2_32_threads_are_refused_by_name(L):
+    """A launch has fewer than 2^32 threads along its grid; one that would need more says so
+    and does not reach the driver."""
+    rows, cols = 1 << 22, 1 << 13  # 2^32 lanes of 8 elements
+    assert L.mx4_quantize(None, P, ecw.DT_BF16, cols, rows, cols, P, P) == UNSUPPORTED
+    assert L.mx4_dequantize(None, P, P, rows, cols, P, ecw.DT_BF16) == UNSUPPORTED
+    strides = (ctypes.c_int64 * 4)(128, 64, 128, 64)
+    c, r = _cache({"kv_heads": 1024, "head_dim": 256}), _rows({"rows": 1 << 18, "batch": 1})
+    assert L.kv4_append(None, c, r, P, P, ecw.DT_BF16, strides) == UNSUPPORTED
+    assert L.kv4_read(None, c, r, P, P, ecw.DT_BF16) == UNSUPPORTED
+    assert L.mx4_gemm(None, P, P, 1 << 20, 7, P, ecw.DT_BF16, 8, 1 << 12, P, ecw.DT_F32) == UNSUPPORTED  # an output a lane
+    assert L.mx4_gemm(None, P, P, 1 << 30, 64, P, ecw.DT_BF16, 64, 1, P, ecw.DT_F32) == UNSUPPORTED     # 16 rows a block
+    assert L.mx4_gemm(None, P, P, 1 << 30, 64, P, ecw.DT_BF16, 64, 1 << 12, P, ecw.DT_F32) == UNSUPPORTED
+    assert L.mx4_gemm_mx4(None, P, P, 1 << 30, 64, P, P, 1 << 20, P, ecw.DT_F32) == UNSUPPORTED
+
+
+def test_attention_of_very_many_rows_is_not_split(L):
+    """The join of splits takes 64 threads for each row and head: hints of short sequences do
+    not have it launched for more of them than a grid holds."""
+    n = ctypes.c_size_t(0)
+    a = {"max_rows": 1, "q_heads": 16, "kv_heads": 2, "table_width": 4096, "starts": P, "batch": 1}
+    for rows, split in ((1 << 20, True), (1 << 22, False)):
+        c, r, t = _cache(a), _rows({**a, "rows": rows}), _attention(a)
+        assert L.kv4_attend_workspace_size(c, r, t, n) == OK and (n.value > 0) == split
