@@ -764,13 +764,23 @@ ecw_status launch_tile(hipStream_t stream, const GemmArgs& a, int y_dtype) {
 template <int ACT>
 ecw_status launch(hipStream_t stream, const GemmArgs& a, int y_dtype) {
   constexpr uint64_t kCus = 256;
-  // A few rows go a block per 16 rows of w, which reads x once for each: more rows and a
-  // short K are better off in tiles (16 rows by 14336 x 4096 22.6 and 10.6 us, 4 rows 13.3;
-  // by 4096 x 14336 19.3 and 23.8).
+  // A few rows go a block per 16 rows of w, which reads x once for each; more than four do
+  // so only where tiles would leave more than half of the CUs without one.  Blocks of 16 rows
+  // and tiles, in us, w from memory where it is large:
+  //                            bf16 x         4-bit x
+  //   16 rows by 4096 x 14336   19.4  22.9     12.7  17.1
+  //   16 rows by 4096 x 4096     8.6   9.4      7.5   7.9
+  //   5 rows by 28672 x 8192    41.3  40.8     34.2  35.3
+  //   16 rows by 28672 x 8192   71.9  39.0     42.3  34.4
+  //   16 rows by 14336 x 4096   20.7  10.3     13.1   9.5
+  //   4 rows by 14336 x 4096    12.7  10.0      9.6   9.2
+  //   4 rows by 28672 x 8192    40.7  41.1     33.4  35.2
+  // (fp16 x is as bf16, but for tiles that unpack in turn: 5 rows by 28672 x 8192 42 and 52, 16
+  // rows 72 and 51, 5 rows by 16384 x 16384 52 and 38.)
   // Operands that start between two words are slow to load (16 rows by 4096 x 14335 54 us,
   // in tiles 35; 4 rows 20).
   const bool words = ACT == kActMX4 || (aligned(a.x, 4) && a.x_stride % 2 == 0);
-  const bool few = a.batch <= 4 || (a.batch <= 16 && words && (tiles(a, 32, 64) < kCus / 2 || a.blocks > 4 * 48));
+  const bool few = a.batch <= 4 || (a.batch <= 16 && words && tiles(a, 32, 64) < kCus / 2);
   if constexpr (ACT == kActMX4) {
     if (few) return launch_few<ACT, true>(stream, a, y_dtype);
     if (tiles(a, 64, 64) <= kCus) return launch_tile<ACT, 1, 4, 4, 1, 3, true, false, 4>(stream, a, y_dtype);

@@ -385,3 +385,17 @@ def test_gemm_every_nan_is_nan_next_to_scales_far_apart(batch):
         x[1, 70].view(torch.int16).fill_(payload)
         y = ecw.mx4_quantize(w).gemm(x)
         assert bool(torch.isnan(y[1]).all()) and bool(torch.isfinite(y[0]).all())
+
+
+@pytest.mark.parametrize("acts", ["bf16", "fp16", "mx4"])
+@pytest.mark.parametrize("batch,rows", [(4, 8300), (5, 8128), (5, 8130), (16, 8300), (17, 8300)])
+def test_gemm_few_rows_by_a_long_k(batch, rows, acts):
+    """Both sides of the rule between blocks of 16 rows and tiles, for long rows of w."""
+    _say("gemm few, long", batch, rows, acts)
+    w = _matrix(rows, 6400, torch.bfloat16, seed=1, spread=0)
+    x = _matrix(batch, 6400, torch.float16 if acts == "fp16" else torch.bfloat16, seed=3, spread=0)
+    t = ecw.mx4_quantize(w)
+    if acts == "mx4":
+        _check_product(w, x, t.gemm(ecw.mx4_quantize(x)), R.rounded(F64(x)))
+    else:
+        _check_product(w, x, t.gemm(x))
