@@ -179,9 +179,9 @@ template <int BYTES>
 __device__ __forceinline__ void to_lds(const void* from, uint32_t to) {
   static_assert(BYTES == 16 || BYTES == 4, "");
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "m0", "memory");
   else
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "m0", "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {
