@@ -172,16 +172,10 @@ __device__ __forceinline__ f32x4 span_product_mx4(f32x4 acc, u32x4 w, uint32_t s
                                                           (int)(sw >> 8 * g));
 }
 
-// Copies 16 (or 4) bytes per lane from global memory to LDS, lane after lane from `to`
-// on, without registers between.  The caller counts them: they are done when
-// `s_waitcnt vmcnt` says so.
-template <int BYTES>
+// Copies 16 bytes per lane from global memory to LDS, lane after lane from `to` on, without
+// registers between.  The caller counts them: they are done when `s_waitcnt vmcnt` says so.
 __device__ __forceinline__ void to_lds(const void* from, uint32_t to) {
-  static_assert(BYTES == 16 || BYTES == 4, "");
-  if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "m0", "memory");
-  else
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "m0", "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "m0", "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -285,7 +279,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int
         const uint32_t half = p * 2 + 1 < spans ? 0 : 64;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          to_lds<16>(from[i] + (uint64_t)p * 128 - (late[i] ? half : 0),
+          to_lds(from[i] + (uint64_t)p * 128 - (late[i] ? half : 0),
                      base + (wave * kTurns + k) * kTurnBytes + i * 1024);
       }
     }
@@ -529,7 +523,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) k_mx4_gemm_tile(GemmArgs a,
       for (int i = 0; i < T::kSLoads; ++i) {
         const uint32_t part = wave + i * T::kWaves;
         if (part < T::kScaleRows / 64)
-          to_lds<16>(sp[i] + s * 4, base + T::kStage * NS + (span / 4 % T::kScalePlaces) * T::kScaleRows * 16 + part * 1024);
+          to_lds(sp[i] + s * 4, base + T::kStage * NS + (span / 4 % T::kScalePlaces) * T::kScaleRows * 16 + part * 1024);
       }
     }
     const uint32_t to = base + stage * T::kStage + kg * T::kSpan;
@@ -555,10 +549,10 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) k_mx4_gemm_tile(GemmArgs a,
         const uint32_t oct = turned(r16 ^ ((part * 4 + g) & 15));
         if ((uint32_t)s * 128 + oct * 8 >= a.cols) from = reinterpret_cast<const uint8_t*>(&zeros16);
       }
-      to_lds<16>(from, to + part * 1024);
+      to_lds(from, to + part * 1024);
     }
 #pragma unroll
-    for (int i = 0; i < T::kWLoads; ++i) to_lds<16>(wp[i] + s * 64, to + T::kX + (wave * T::kWLoads + i) * 1024);
+    for (int i = 0; i < T::kWLoads; ++i) to_lds(wp[i] + s * 64, to + T::kX + (wave * T::kWLoads + i) * 1024);
   };
 
   f32x4 acc[TN][TM];
