@@ -710,7 +710,6 @@ __global__ void __launch_bounds__(64 * kJoinWaves) k_kv4_join(const float* __res
   float o[N] = {};
 #pragma unroll
   for (int k = 0; k < EACH; ++k) {
-#pragma unroll 8
     for (uint32_t s = 64 * k + first; s < min(splits, 64u * k + 64); s += per) {
       const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f[k]), s % 64));
       const float* p = part + (s * all + at) * D + lane * N;
