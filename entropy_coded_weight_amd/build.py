@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -24,13 +25,17 @@ BIND = os.path.join(HERE, "_mx4.so")
 
 
 def _bind_flags():
-    import sysconfig
-
+    """Compiler and linker arguments of the binding, or the header that is missing for it."""
     import torch
     from torch.utils.cpp_extension import include_paths
+    python, rocm = sysconfig.get_paths()["include"], f"{os.environ.get('ROCM_PATH', '/opt/rocm')}/include"
+    dirs = [python, rocm, *include_paths()]
+    for header in ("Python.h", "hip/hip_runtime.h", "torch/csrc/autograd/python_variable.h"):
+        if not any(os.path.exists(os.path.join(d, header)) for d in dirs):
+            return header
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return (["-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-             "-D__HIP_PLATFORM_AMD__=1", f"-I{sysconfig.get_paths()['include']}", f"-I{os.environ.get('ROCM_PATH', '/opt/rocm')}/include"]
+             "-D__HIP_PLATFORM_AMD__=1", f"-I{python}", f"-I{rocm}"]
             + [f"-isystem{p}" for p in include_paths()],
             [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"])
 
@@ -62,7 +67,13 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs, "-lpthread"], verbose)
     os.replace(tmp, LIB)
-    flags, libs = _bind_flags()
+    found = _bind_flags()
+    if isinstance(found, str):  # libecw.so does without it; the 4-bit calls from Python say what is missing
+        if os.path.exists(BIND):
+            os.remove(BIND)  # of another state of the sources
+        sys.stderr.write(f"{BIND} not built: {found} not found; the 4-bit calls from Python need it\n")
+        return LIB
+    flags, libs = found
     _run(["g++", *flags, os.path.join(CSRC, "mx4_bind.cpp"), "-o", BIND + ".tmp", *libs], verbose)
     os.replace(BIND + ".tmp", BIND)
     return LIB

@@ -1,6 +1,8 @@
 """Refusals of the 4-bit entry points, through the C ABI and without a GPU: a bad call
 returns its status before anything is launched."""
 import ctypes
+import os
+import sysconfig
 
 import pytest
 import torch
@@ -172,3 +174,19 @@ def test_attention_of_very_many_rows_is_not_split(L):
     for rows, split in ((1 << 20, True), (1 << 22, False)):
         c, r, t = _cache(a), _rows({**a, "rows": rows}), _attention(a)
         assert L.kv4_attend_workspace_size(c, r, t, n) == OK and (n.value > 0) == split
+
+
+def test_build_without_python_headers_still_gives_the_library(monkeypatch, tmp_path, capsys):
+    """libecw.so needs neither Python's headers nor torch's; without them only the binding of
+    the 4-bit calls is left out, with a word."""
+    from entropy_coded_weight_amd import build
+    ran, bind, paths = [], tmp_path / "_mx4.so", sysconfig.get_paths()
+    bind.write_text("of an older build")
+    monkeypatch.setattr(build, "BIND", str(bind))
+    monkeypatch.setattr(build, "_run", lambda cmd, verbose: ran.append(cmd))
+    monkeypatch.setattr(os, "replace", lambda a, b: ran.append([a, b]))
+    monkeypatch.setattr(sysconfig, "get_paths", lambda *a, **k: {**paths, "include": str(tmp_path)})
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libecw.so"))
+    assert build.build() == build.LIB
+    assert [build.LIB + ".tmp", build.LIB] in ran and not any("mx4_bind.cpp" in part for cmd in ran for part in cmd)
+    assert not bind.exists() and "Python.h" in capsys.readouterr().err
