@@ -8,6 +8,7 @@ rounding of 2^-23 of sum |q k| for each of the D / 32 instructions and the 64 ad
 inside, and 2^-18 for the exponential's argument and result (scores here stay under
 2^5, half an fp32 step of 2^-19 there).  The sums over tokens add 2^-23 for each of
 the T / 32 tiles and 128 more.  Then half a step of the output type."""
+import threading
 from types import SimpleNamespace
 
 import numpy as np
@@ -535,3 +536,75 @@ def test_given_outputs_count_as_written():
     bed.cache.attend(q, bed.table, lens, out=held)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+@pytest.mark.parametrize("dim,group,n", [(64, 8, 1), (64, 8, 40), (128, 4, 1), (128, 4, 40), (256, 2, 1), (256, 2, 9)])
+def test_fp16_weights_are_fp16(dim, group, n):
+    """With an fp16 query the softmax weights have fp16's bits: half a step, 2^-11, of each in
+    the sum over values and in the weights' own sum, and fp16's smallest step, 2^-25 against
+    a largest weight of 2^7 or more, of each token.  The other terms as in Bed.check."""
+    _say("attend fp16 weights", dim, group, n)
+    bed = Bed([1027, 60], 2, dim, dtype=FP16)
+    q = _normal(78, 2 * n, 2 * group, dim, dtype=FP16, scale=1.5)
+    got, qd = F64(bed.cache.attend(q, bed.table, I32(bed.lens))), F64(q)
+    for b, length in enumerate(bed.lens):
+        kv, vv = R.rounded(F64(bed.k[b])), R.rounded(F64(bed.v[b]))
+        want, mag, dot = R.attend_rows(qd[b * n:b * n + n], np.arange(length - n, length), kv, vv, bed.there[b],
+                                       dim ** -0.5, 0, 0)
+        score = (dim / 32 + 64) * 2.0 ** -23 * dot + 2.0 ** -18
+        tol = (2 * 2.0 ** -11 + 2 * score + (length / 32 + 128) * 2.0 ** -23) * mag + 2 * length * 2.0 ** -32 * np.abs(vv).max()
+        tol = tol + 2.0 ** -11 * (np.abs(want) + tol) + 2.0 ** -25
+        err = np.abs(got[b * n:b * n + n] - want)
+        assert (err <= tol).all(), f"sequence {b}: worst {(err / tol).max()}"
+
+
+def test_graph_replays_append_keys_and_values():
+    _say("append graph")
+    bed = Bed([300, 77], 2, 128)
+    lens, k, v = I32(bed.lens), _normal(86, 2, 2, 128), _normal(85, 2, 2, 128)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        lens -= 1
+        bed.cache.append(k, v, bed.table, lens)
+        back = bed.cache.read(bed.table, lens, 2)
+    kept = [], []
+    for step in range(4):
+        k.copy_(_normal(20 + step, 2, 2, 128))
+        v.copy_(_normal(40 + step, 2, 2, 128))
+        g.replay()
+        torch.cuda.synchronize()
+        for got, new, rows in zip(back, (k, v), kept):
+            rows.insert(0, R.rounded(F64(new)))
+            assert np.array_equal(F64(got), rows[0])
+    tail = bed.cache.read(bed.table, I32(bed.lens), 10)  # the last five: four new ones and the old last
+    for got, old, rows in zip(tail, (bed.k, bed.v), kept):
+        for b in range(2):
+            want = [*(r[b] for r in rows), R.rounded(F64(old[b][-1]))]
+            assert np.array_equal(F64(got).reshape(2, 5, 2, 128)[b], np.stack(want))
+
+
+def test_two_streams_and_two_threads_at_once():
+    """Calls share nothing: a thread each with its stream and cache gives what it gives alone."""
+    _say("attend two threads")
+    beds = [Bed([5000, 300], 2, 128, seed=s) for s in (0, 1)]
+    qs = [_normal(70 + s, 2, 8, 128) for s in (0, 1)]
+    alone = [b.cache.attend(q, b.table, I32(b.lens)) for b, q in zip(beds, qs)]
+    lens = [I32(b.lens) for b in beds]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got[i].append(beds[i].cache.attend(qs[i], beds[i].table, lens[i]))
+            stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in (0, 1):
+        assert len(got[i]) == 20 and all(torch.equal(o, alone[i]) for o in got[i])
