@@ -172,15 +172,18 @@ __global__ void __launch_bounds__(256) k_kv4_read(Cache c, Batch t, void* __rest
 // With a bf16 query keys, values and weights are bf16; with an fp16 query fp16, which
 // holds keys and values exactly between scales of 2^-23 and 2^13, all that fp16 keys and
 // values can have.  Smaller ones round to multiples of 2^-24, larger ones count as NaN.
+// Rounding the weights to q's type is what the matrix instruction takes; next to the
+// output's own rounding to it, errors against 64 bits are 1.1 to 1.35 times those of weights
+// in 32 bits.
 //
 // Four waves of a block take tiles of 32 tokens in turn, straight into registers, the next
 // one asked for while one is multiplied.  For single tokens bound by memory (32 sequences
 // up to 32768 tokens, 8 heads of 128 dimensions: 195 us, 4.4 TB/s of cache), for short ones
 // by the latency of lengths, page table and pages in turn (1001 tokens 5.5 us, and 3.9 for
 // the join), for many rows by vector instructions, which unpack 4-bit values and take
-// exponentials (512 rows of 32 heads behind 16384 tokens 231 us, 590 TFLOP/s).  Blocks whose
-// waves share a tile's operands through LDS took 257 us there: the copies, one tile ahead,
-// were waited for.
+// exponentials (512 fp16 rows of 32 heads behind 16384 tokens 204 us, 660 TFLOP/s, bf16 220).
+// Blocks whose waves share a tile's operands through LDS took 257 us there when these took
+// 210: the copies, one tile ahead, were waited for.
 struct AttendArgs {
   Cache c;
   Batch t;
@@ -512,7 +515,10 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, f32x4 o, float
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
-// Blocks of four waves that a CU's registers hold.
+// Blocks of four waves that a CU is given.  Its registers hold no more, but for heads of 64
+// with two query tiles: three fit, and with three a prompt of 512 rows behind 16384 tokens
+// takes 157 us and with two 158, 40 rows of 2 sequences over 30000 tokens 57 and 61, but 615
+// rows of 16 sequences over 3211 tokens 40 and 32, for then two tiles are taken there.
 constexpr int at_once(int dim, int nq) { return nq == 2 || dim == 256 ? 2 : dim == 128 ? 3 : 4; }
 
 // A row's output: element 4 d + r of the lane (o[n][d][r]) is dimension 2 NB (4 g + r) + d.
@@ -790,7 +796,8 @@ bool row_grid(const ecw_kv4* c, const ecw_kv4_rows* r, uint32_t* grid) {
 }
 
 constexpr float kLog2E = 1.44269504088896f;
-constexpr uint64_t kChunk = 12;  // tiles of 32 tokens of a split at least, for its four waves
+// tiles of 32 tokens of a split, for its four waves: no fewer, but where CUs are idle (plan_with)
+constexpr uint64_t kChunk = 12;
 
 // How an attention call is cut up: query tiles of 16 nq rows, and splits of each
 // sequence's tokens.
@@ -828,12 +835,12 @@ Plan plan_with(uint32_t nq, uint64_t rows, uint64_t tiles, const ecw_kv4* c, uin
 }
 
 // One or two tiles of rows a wave: two take 1.6 times as long for a tile of keys, and half
-// the blocks (512 rows of 32 heads behind 16384 tokens 220 us, one 283; 20 rows of 256 heads
-// of sequences over 16000 tokens 158 and 189), but fewer blocks may leave CUs idle (615
-// rows of dimension 64 over 3211 tokens, 16 sequences: 41 and 33 us; 48 rows over 8000
-// tokens, 64 heads of sequences: 48 and 40; 20 rows over 2935 tokens, 6 of them: 13.0 and
-// 10.7).  Four take all registers (512 rows behind 16384 tokens 275 and 216 us), and so do
-// two of dimension 256 (300 rows of 6 heads behind 16000 tokens 92 us, one 81).
+// the blocks (512 rows of 32 heads behind 16384 tokens 220 us, one 278; 20 rows of 256 heads
+// of sequences over 16000 tokens 155 and 185), but fewer blocks may leave CUs idle (615
+// rows of dimension 64 over 3211 tokens, 16 sequences: 40 and 32 us; 48 rows over 8000
+// tokens, 64 heads of sequences: 46 and 39; 20 rows over 2935 tokens, 6 of them: 13.4 and
+// 10.8).  Four take all registers (512 rows behind 16384 tokens 275 us), and so do two of
+// dimension 256 (300 rows of 6 heads behind 16000 tokens 92 us, one 81).
 Plan plan_of(const ecw_kv4* c, const ecw_kv4_rows* r, const ecw_kv4_attention* at) {
   const uint64_t group = at->q_heads / c->kv_heads;
   const uint64_t each = at->max_rows ? (at->max_rows < r->rows ? at->max_rows : r->rows) : (r->rows + r->batch - 1) / r->batch;

@@ -200,8 +200,8 @@ __device__ __forceinline__ u32x4 moved_down(u32x4 v, uint32_t elements) {
 // read whole lines: as operands they would be 16-byte pieces of 16 rows.  16 bytes at
 // piece p of row r's 8 lie at p ^ stirred(r), so that the 16 lanes that LDS serves together
 // meet no bank twice.  The first turn's x is asked for before w, later turns' one turn
-// ahead: behind w in a CU's queue, x took 3 of 11.8 us for one row by 14336 x 4096 (10.7
-// us; 31 MB of w).  Bound by reading w.
+// ahead: behind w in a CU's queue, x took 1 us more for one row by 14336 x 4096 (9.2 us with
+// the 31 MB of w in the last-level cache, 12.0 from memory).  Bound by reading w.
 __device__ __forceinline__ uint32_t stirred(uint32_t r) { return ((r >> 1) + 2) & 7; }
 
 constexpr uint32_t kTurns = 4;             // pairs of spans that a wave has in LDS
@@ -209,7 +209,7 @@ constexpr uint32_t kTurnBytes = 16 * 128;  // 16 rows of w
 constexpr uint32_t kFewWaves = 16;         // at most
 
 // NEAR: 16-bit x ends within 2^31 bytes.  Its rows may start at any element (one row by
-// 14336 x 4095: 10.3 us).
+// 14336 x 4095: 9.0 and 12.0 us too).
 template <int ACT, bool NEAR>
 __global__ void __launch_bounds__(64 * kFewWaves) k_mx4_gemm_few(GemmArgs a, int y_dtype) {
   extern __shared__ __align__(16) uint8_t lds[];  // each wave's turns, then (over them) the sums
@@ -389,9 +389,10 @@ __device__ __forceinline__ uint32_t shifted(uint32_t r) { return (0u - (r >> 2))
 // and 4 42, 28 and 24).
 //
 // The large tiles are bound by LDS, which serves operands for about as long as the matrix
-// instructions take and the copies' writes next to them (bf16 x, 1003 rows by 4096 x 4096
-// 39 us, 860 TFLOP/s; 4-bit x, 4096 rows by 14336 x 4096 174 us, 2.76 PFLOP/s, of which the
-// outputs' stores are a third).
+// instructions take and the copies' writes next to them (1003 rows by 4096 x 4096, in a
+// graph: bf16 x 41 us, 820 TFLOP/s, fp16 50, whose spans' scales are vector instructions;
+// 4-bit x, 4096 rows by 14336 x 4096 174 us, 2.76 PFLOP/s, of which the outputs' stores are
+// a third).
 template <int ACT, int WM, int WN, int TM, int TN, int NS, bool EARLY, bool LOOSE, int KG>
 struct Tiles {
   static constexpr bool kX4 = ACT == kActMX4;

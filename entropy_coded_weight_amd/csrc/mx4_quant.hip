@@ -23,8 +23,8 @@ ecw_status launched(const char* what) noexcept {
 
 // One lane per 8 elements, four lanes per block, so that a wave reads 1 KiB of 16-bit
 // input in one load and writes 256 bytes of codes.  Bound by memory (14336 x 4096 bf16
-// 27.5 us, 5.4 TB/s; 4096 x 14335, rows at any element, 31 us; one row of 4096 1.8 us, the
-// latency of a load and a store).
+// 27.5 us, 5.4 TB/s; 4096 x 14335, rows at any element, 31 us; one row of 4096 1.5 to 1.8 us,
+// the latency of a load and a store).
 template <int DT>
 __global__ void __launch_bounds__(256) k_mx4_quantise(const void* __restrict__ x, int64_t stride, uint32_t rows,
                                                       uint32_t cols, uint32_t octs, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {

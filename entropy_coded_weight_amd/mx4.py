@@ -2,7 +2,7 @@
 
 The format and the operations are described in include/ecw.h; operands are checked and
 results allocated in the native binding (csrc/mx4_bind.cpp).  Inference only: no call
-records a gradient.
+records a gradient, and an input that requires one is used as its values.
 
     w = mx4_quantize(weights)                  # MX4Tensor, 4.25 bits per element
     y = w.gemm(x)                              # x: fp16/bf16 [batch, cols] -> fp32 [batch, rows]
@@ -12,8 +12,8 @@ records a gradient.
     cache.append(k, v, page_table, lens)       # the last rows of each sequence
     o = cache.attend(q, page_table, lens)      # causal attention over the cache
 
-Work runs on the current stream of the operands' device, or on `stream`; results are
-allocated there.  Whoever passes a stream orders it after the producers of the operands.
+Work runs on the current stream of the operands' device, or on `stream`, one of the same
+device; results are allocated there.  Whoever passes a stream orders it after the producers of the operands.
 """
 from __future__ import annotations
 
@@ -175,8 +175,9 @@ class KV4Cache:
 
         q fp16/bf16 [rows, q_heads, head_dim]; q_heads a multiple of kv_heads.  A row at
         position p sees tokens up to p; with a window only the last `window` of them and
-        the sequence's first `sinks`.  A row that sees nothing gives zeros.  scale:
-        head_dim ** -0.5.  max_rows, max_len: the most rows and tokens of one sequence, if
+        the sequence's first `sinks`.  A row that sees nothing gives zeros.  Softmax weights
+        are rounded to q's type, sums are fp32; with q in fp16, keys and values past fp16's
+        range count as NaN.  scale: head_dim ** -0.5.  max_rows, max_len: the most rows and tokens of one sequence, if
         the host knows them; they shape the launch, not the result's meaning."""
         if stream is not None:
             return _on(stream, (self.data, q, page_table, lens, starts, out),

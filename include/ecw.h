@@ -432,9 +432,12 @@ ecw_status kv4_append(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
 ecw_status kv4_read(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, void* k, void* v, int dtype);
 /* o [rows][q_heads][head_dim] = softmax(scale q k^T) v over the visible tokens, causal
  * inside a sequence's rows; q and o fp16 or bf16, q's strides in elements.  A row that
- * sees nothing gives zeros.  With q in fp16 the cache's values are used as fp16 numbers:
- * exact if they were appended as fp16; blocks past its range count as NaN.  The workspace
- * need not be cleared. */
+ * sees nothing gives zeros; a NaN block of a key that a row sees makes the row NaN, one of a
+ * value its 32 dimensions, whatever the weight.  Scores, softmax state and sums are fp32; the softmax's weights are rounded to
+ * q's type (bf16: half a step is 2^-8 of each, fp16 2^-11) and summed as rounded.  With q in
+ * fp16 the cache's keys and values are used as fp16 numbers: exact if they were appended as
+ * fp16, else rounded to multiples of 2^-24; key and value blocks with a scale over 2^13,
+ * past its range, count as NaN.  The workspace need not be cleared. */
 ecw_status kv4_attend_workspace_size(const ecw_kv4* cache, const ecw_kv4_rows* rows, const ecw_kv4_attention* at,
                                      size_t* bytes);
 ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_rows* rows, const ecw_kv4_attention* at,
