@@ -492,4 +492,5 @@ class CompressedTensor:
         return sym, w, st[: self.t.n_tiles]
 
 
-from .mx4 import KV4Cache, MX4Tensor, mx4_quantize  # noqa: E402,F401  (uses the binding above)
+from .fp8 import FP8Tensor, Rotary, fp8_quantize, rms_norm  # noqa: E402,F401  (uses the binding above)
+from .mx4 import KV4Cache, MX4Tensor, mx4_quantize  # noqa: E402,F401

@@ -5,6 +5,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -20,7 +21,8 @@ HIP_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-mcode-object-version=5", "-mllvm", "-amdgpu-kernarg-preload-count=11", "-Wall", "-Wno-unused-result",
              f"-I{ROOT}"]
-# the torch binding of the 4-bit calls: host code against torch's headers
+# the torch bindings, of the 4-bit calls and (_fp8.so next to it) of the 8-bit calls, the norm and
+# the rotary positions: host code against torch's headers
 BIND = os.path.join(HERE, "_mx4.so")
 
 
@@ -40,6 +42,8 @@ def _bind_flags():
             [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"])
 
 
+HIP_SOURCES = ("ecw_kernels.hip", "ecw_probes.hip", "mx4_quant.hip", "mx4_gemm.hip", "kv4.hip", "fp8_quant.hip",
+               "fp8_gemm.hip", "rms_norm.hip", "rotary.hip")
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{ROOT}"]
 
 
@@ -59,23 +63,28 @@ def build(verbose: bool = False) -> str:
     os.makedirs(bdir, exist_ok=True)
     host_o = os.path.join(bdir, "ecw_host.o")
     _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "ecw_host.cpp"), "-o", host_o], verbose)
-    objs = [host_o]
-    for src in ("ecw_kernels.hip", "ecw_probes.hip", "mx4_quant.hip", "mx4_gemm.hip", "kv4.hip"):
+    def hip(src):
         obj = os.path.join(bdir, src.replace(".hip", ".o"))
         _run([HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objs = [host_o, *pool.map(hip, HIP_SOURCES)]
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs, "-lpthread"], verbose)
     os.replace(tmp, LIB)
     found = _bind_flags()
-    if isinstance(found, str):  # libecw.so does without it; the 4-bit calls from Python say what is missing
-        if os.path.exists(BIND):
-            os.remove(BIND)  # of another state of the sources
-        sys.stderr.write(f"{BIND} not built: {found} not found; the 4-bit calls from Python need it\n")
+    binds = [(BIND, "mx4_bind.cpp"), (os.path.join(os.path.dirname(BIND), "_fp8.so"), "fp8_bind.cpp")]
+    if isinstance(found, str):  # libecw.so does without them; the calls from Python say what is missing
+        for bind, _ in binds:
+            if os.path.exists(bind):
+                os.remove(bind)  # of another state of the sources
+            sys.stderr.write(f"{bind} not built: {found} not found; its calls from Python need it\n")
         return LIB
     flags, libs = found
-    _run(["g++", *flags, os.path.join(CSRC, "mx4_bind.cpp"), "-o", BIND + ".tmp", *libs], verbose)
-    os.replace(BIND + ".tmp", BIND)
+    for bind, src in binds:
+        _run(["g++", *flags, os.path.join(CSRC, src), "-o", bind + ".tmp", *libs], verbose)
+        os.replace(bind + ".tmp", bind)
     return LIB
 
 

@@ -18,13 +18,11 @@ device; results are allocated there.  Whoever passes a stream orders it after th
 from __future__ import annotations
 
 import ctypes
-import os
 
 import torch
 
-from . import EcwError, _check, lib
-
-_BIND_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mx4.so")
+from . import _check, lib
+from ._binding import native, on
 
 
 class _Cache(ctypes.Structure):
@@ -32,35 +30,18 @@ class _Cache(ctypes.Structure):
         "pages", "kv_heads", "head_dim", "page_tokens")]
 
 
-_bound = None
+_ready = None
 
 
 def _native():
     """The binding, with the library loaded (raises if they have not been built)."""
-    global _bound
-    if _bound is None:
+    global _ready
+    if _ready is None:
         L = lib()
-        if not os.path.exists(_BIND_PATH):
-            raise ImportError(f"{_BIND_PATH} missing: run __graft_entry__.build() (or "
-                              "python entropy_coded_weight_amd/build.py) first")
-        from . import _mx4
         L.kv4_bytes.argtypes = [ctypes.POINTER(_Cache), ctypes.POINTER(ctypes.c_size_t)]
         L.kv4_bytes.restype = ctypes.c_int
-        _mx4.init(L._name, EcwError)
-        _bound = _mx4
-    return _bound
-
-
-def _on(stream, tensors, call):
-    """call() with `stream` current; the tensors live on until its work is done."""
-    tensors = [t for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda]
-    for t in tensors:  # work goes to the tensors' device, whose current stream would be another one
-        if t.device != stream.device:
-            raise ValueError(f"the stream is on {stream.device}, an operand on {t.device}")
-    with torch.cuda.stream(stream):
-        for t in tensors:
-            t.record_stream(stream)
-        return call()
+        _ready = native("_mx4")
+    return _ready
 
 
 class MX4Tensor:
@@ -97,7 +78,7 @@ class MX4Tensor:
     def dequantize(self, dtype=torch.float16, out=None, stream=None) -> torch.Tensor:
         """The values as a dense [rows, cols] matrix: exact in bfloat16 and float32."""
         if stream is not None:
-            return _on(stream, (self.codes, self.scales, out), lambda: self.dequantize(dtype, out))
+            return on(stream, (self.codes, self.scales, out), lambda: self.dequantize(dtype, out))
         return _native().dequantize(self.codes, self.scales, self.cols, dtype, out)
 
     def gemm(self, x, y=None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
@@ -105,7 +86,7 @@ class MX4Tensor:
         [batch, cols]; y [batch, rows], fp32 unless out_dtype (fp16, bf16) says otherwise."""
         if stream is not None:
             used = (x.codes, x.scales) if isinstance(x, MX4Tensor) else (x,)
-            return _on(stream, (self.codes, self.scales, y, *used), lambda: self.gemm(x, y, out_dtype))
+            return on(stream, (self.codes, self.scales, y, *used), lambda: self.gemm(x, y, out_dtype))
         if isinstance(x, MX4Tensor):
             return _native().gemm_mx4(self.codes, self.scales, self.cols, x.codes, x.scales, x.cols, y, out_dtype)
         return _native().gemm(self.codes, self.scales, self.cols, x, y, out_dtype)
@@ -115,7 +96,7 @@ def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None, stream=None) -> 
     """x fp16/bf16/fp32 [rows, cols] (or [cols]), rows at any stride, as an MX4Tensor."""
     if stream is not None:
         used = (x,) if out is None else (x, out.codes, out.scales)
-        return _on(stream, used, lambda: mx4_quantize(x, out))
+        return on(stream, used, lambda: mx4_quantize(x, out))
     if out is not None:
         if not isinstance(x, torch.Tensor) or out.shape != (tuple(x.shape) if x.dim() == 2 else (1, *x.shape)):
             raise ValueError(f"out is {out.shape}, x {getattr(x, 'shape', x)}")
@@ -157,7 +138,7 @@ class KV4Cache:
         """k, v fp16/bf16/fp32 [rows, kv_heads, head_dim] into the cache; rows without a
         page are dropped.  Calls on different streams that write the same pages race."""
         if stream is not None:
-            return _on(stream, (self.data, k, v, page_table, lens, starts),
+            return on(stream, (self.data, k, v, page_table, lens, starts),
                        lambda: self.append(k, v, page_table, lens, starts))
         return _native().append(*self._as_args, k, v, page_table, lens, starts)
 
@@ -165,7 +146,7 @@ class KV4Cache:
         """The values of the last rows of each sequence as (k, v) [rows, kv_heads, head_dim];
         zeros for a row without a page."""
         if stream is not None:
-            return _on(stream, (self.data, page_table, lens, starts),
+            return on(stream, (self.data, page_table, lens, starts),
                        lambda: self.read(page_table, lens, rows, starts, dtype))
         return _native().read(*self._as_args, page_table, lens, starts, rows, dtype)
 
@@ -180,7 +161,7 @@ class KV4Cache:
         range count as NaN.  scale: head_dim ** -0.5.  max_rows, max_len: the most rows and tokens of one sequence, if
         the host knows them; they shape the launch, not the result's meaning."""
         if stream is not None:
-            return _on(stream, (self.data, q, page_table, lens, starts, out),
+            return on(stream, (self.data, q, page_table, lens, starts, out),
                        lambda: self.attend(q, page_table, lens, starts, max_rows, max_len, window, sinks, scale, out))
         return _native().attend(*self._as_args, q, page_table, lens, starts, max_rows, max_len, window, sinks, scale,
                                 out)

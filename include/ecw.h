@@ -444,6 +444,72 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
                       const void* q, int dtype, int64_t q_row, int64_t q_head, void* o, void* workspace,
                       size_t workspace_bytes);
 
+/*
+ * The block-scaled 8-bit format (FP8): matrices at 8.0625 bits per element, for the products
+ * of layers whose activations need more than 4 bits.
+ *
+ * 128 neighbouring columns of a row share a scale 2^s, stored as the byte s + 127; an element
+ * is an E4M3 number (OCP: largest 448, no infinities) times the scale.
+ *   s = the smallest with largest magnitude <= 448 * 2^s, held to -117..119 (an all-zero block: 0)
+ *   elements round to nearest, ties to even; magnitudes over 448 (at s = 119 only) become 448
+ * A block with an infinity or a NaN has the byte 255, its codes are NaN.  Zeros past the last
+ * column fill a row up to a multiple of 128 columns.
+ *   codes  [rows][ceil(cols / 128) * 128] bytes    scales [rows][ceil(cols / 2048) * 16] bytes
+ * both 16-byte aligned device memory.  No call needs workspace; calls with rows or batch of
+ * zero launch nothing.
+ */
+
+/* x [rows][cols] fp16, bf16 or fp32, x_stride elements apart -> codes, scales.  With a gate
+ * (same type and shape; else NULL) it is silu(gate) * x that is quantised, computed in fp32:
+ * silu(g) = g / (1 + e^-g), zero below g = -88. */
+ecw_status fp8_quantize(ecw_stream stream, const void* x, int dtype, int64_t x_stride, const void* gate,
+                        int64_t gate_stride, uint32_t rows, uint32_t cols, void* codes, void* scales);
+/* The values as a dense [rows][cols] matrix: exact in fp32 and bf16, rounded to nearest
+ * even in fp16 (infinite past its range). */
+ecw_status fp8_dequantize(ecw_stream stream, const void* codes, const void* scales, uint32_t rows, uint32_t cols,
+                          void* out, int out_dtype);
+/* y [batch][rows] (fp32, fp16 or bf16) = x w^T with both in the format; products exact, sums
+ * in fp32, one rounding into y. */
+ecw_status fp8_gemm(ecw_stream stream, const void* w_codes, const void* w_scales, uint32_t rows, uint32_t cols,
+                    const void* x_codes, const void* x_scales, uint32_t batch, void* y, int y_dtype);
+
+/* y = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual, and h as the new
+ * residual.  h is fp32 and rounded once, into residual_out; y is made of the unrounded h.
+ * Strides in elements; y is dense, in a float type or in the 8-bit format (y its codes,
+ * y_scales its scales).  residual_out may be residual itself, with the same stride. */
+typedef struct {
+  const void* x;           /* [rows][cols], rows x_stride apart */
+  const void* residual;    /* nullable, in x's type or fp32 */
+  const void* weight;      /* [cols], nullable: ones */
+  void* residual_out;      /* with a residual, in its type */
+  void* y;
+  void* y_scales;          /* for ECW_DT_FP8_E4M3 */
+  int64_t x_stride, residual_stride, residual_out_stride;
+  uint32_t rows, cols;     /* at most 32768 columns */
+  int x_dtype, residual_dtype, weight_dtype, y_dtype;
+  float eps;               /* finite, not negative */
+} ecw_rms_norm;
+ecw_status rms_norm(ecw_stream stream, const ecw_rms_norm* norm);
+
+/* Rotary positions: pair j of a head's first rotary_dim dimensions (dimensions j and
+ * j + rotary_dim / 2, or with `neighbours` 2 j and 2 j + 1) is turned by the angle
+ * positions[axis_of[j]][row] * frequency j, and multiplied by scale; the dimensions behind
+ * stay.  freqs: frequencies as fractions of a turn per position, in 2^-64, modulo a turn.
+ * q_out and k_out may be q and k, with the same strides.  The sine and cosine are within 2^-23,
+ * products fp32, one rounding into the output. */
+typedef struct {
+  const void *q, *k;             /* [rows][heads][head_dim], strides of rows and heads in elements */
+  void *q_out, *k_out;
+  const void* positions;         /* int32 (int64 if wide_positions) [axes][rows], axes axis_stride apart */
+  const void* freqs;             /* device uint64 [rotary_dim / 2] */
+  const void* axis_of;           /* device uint8 [rotary_dim / 2]; past the last axis: the last */
+  int64_t q_row, q_head, k_row, k_head, q_out_row, q_out_head, k_out_row, k_out_head, axis_stride;
+  uint32_t rows, q_heads, k_heads, head_dim, rotary_dim, axes;
+  int dtype, neighbours, wide_positions;
+  float scale;
+} ecw_rotary;
+ecw_status rotary_apply(ecw_stream stream, const ecw_rotary* rotary);
+
 #ifdef __cplusplus
 }
 #endif
