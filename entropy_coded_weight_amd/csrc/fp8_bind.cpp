@@ -9,6 +9,7 @@ struct Api {
   decltype(&fp8_quantize) quantize;
   decltype(&fp8_dequantize) dequantize;
   decltype(&fp8_gemm) gemm;
+  decltype(&fp8_gemm_workspace_size) workspace;
   decltype(&rms_norm) norm;
   decltype(&rotary_apply) rotary;
 } api;
@@ -90,8 +91,13 @@ PyObject* py_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = a[6] == Py_None ? dtype(a[7], "out_dtype") : tensor(a[6], "y").scalar_type();
     const int yd = float_type(type, "y");
     const at::Tensor y = output(a[6], codes, {xc.size(0), rows}, type, "y");
+    const uint32_t batch = size32(xc.size(0), "batch");
+    size_t bytes = 0;
+    check(api.workspace((uint32_t)rows, (uint32_t)cols, batch, yd, &bytes), "fp8_gemm_workspace_size");
+    at::Tensor ws;
+    if (bytes) ws = at::empty({(int64_t)bytes}, codes.options());
     check(api.gemm(stream_of(codes.device()), codes.data_ptr(), scales.data_ptr(), (uint32_t)rows, (uint32_t)cols,
-                   xc.data_ptr(), xs.data_ptr(), size32(xc.size(0), "batch"), y.data_ptr(), yd),
+                   xc.data_ptr(), xs.data_ptr(), batch, y.data_ptr(), yd, bytes ? ws.data_ptr() : nullptr, bytes),
           "fp8_gemm");
     return THPVariable_Wrap(y);
   });
@@ -259,8 +265,8 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // init(path of libecw.so, EcwError)
 PyObject* py_init(PyObject*, PyObject* args) {
   return load_calls(args, {{"fp8_quantize", (void**)&api.quantize}, {"fp8_dequantize", (void**)&api.dequantize},
-                           {"fp8_gemm", (void**)&api.gemm},         {"rms_norm", (void**)&api.norm},
-                           {"rotary_apply", (void**)&api.rotary}});
+                           {"fp8_gemm", (void**)&api.gemm},         {"fp8_gemm_workspace_size", (void**)&api.workspace},
+                           {"rms_norm", (void**)&api.norm},         {"rotary_apply", (void**)&api.rotary}});
 }
 
 PyMethodDef methods[] = {FAST(quantize), FAST(dequantize), FAST(gemm), FAST(rms_norm), FAST(rotary),

@@ -455,8 +455,7 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
  * A block with an infinity or a NaN has the byte 255, its codes are NaN.  Zeros past the last
  * column fill a row up to a multiple of 128 columns.
  *   codes  [rows][ceil(cols / 128) * 128] bytes    scales [rows][ceil(cols / 2048) * 16] bytes
- * both 16-byte aligned device memory.  No call needs workspace; calls with rows or batch of
- * zero launch nothing.
+ * both 16-byte aligned device memory.  Calls with rows or batch of zero launch nothing.
  */
 
 /* x [rows][cols] fp16, bf16 or fp32, x_stride elements apart -> codes, scales.  With a gate
@@ -469,9 +468,15 @@ ecw_status fp8_quantize(ecw_stream stream, const void* x, int dtype, int64_t x_s
 ecw_status fp8_dequantize(ecw_stream stream, const void* codes, const void* scales, uint32_t rows, uint32_t cols,
                           void* out, int out_dtype);
 /* y [batch][rows] (fp32, fp16 or bf16) = x w^T with both in the format; products exact, sums
- * in fp32, one rounding into y. */
+ * in fp32, one rounding into y.  With a 16-bit y and more than a few rows of x up to 16
+ * neighbouring products are added with 12 fraction bits under the largest one's power of two
+ * before they go into the fp32 sum: 1.5e-5 to 7e-5 of the result (2-norm), a small part of
+ * what rounding it to 16 bits takes.  The workspace need not be cleared; it is the call's
+ * until its work is done. */
+ecw_status fp8_gemm_workspace_size(uint32_t rows, uint32_t cols, uint32_t batch, int y_dtype, size_t* bytes);
 ecw_status fp8_gemm(ecw_stream stream, const void* w_codes, const void* w_scales, uint32_t rows, uint32_t cols,
-                    const void* x_codes, const void* x_scales, uint32_t batch, void* y, int y_dtype);
+                    const void* x_codes, const void* x_scales, uint32_t batch, void* y, int y_dtype, void* workspace,
+                    size_t workspace_bytes);
 
 /* y = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual, and h as the new
  * residual.  h is fp32 and rounded once, into residual_out; y is made of the unrounded h.

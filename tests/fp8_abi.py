@@ -25,7 +25,8 @@ def _lib():
     L = ctypes.CDLL(ecw.lib()._name)  # a handle of its own: the binding's signatures stay as they are
     L.fp8_quantize.argtypes = [_vp, _vp, _i32, _i64, _vp, _i64, _u32, _u32, _vp, _vp]
     L.fp8_dequantize.argtypes = [_vp, _vp, _vp, _u32, _u32, _vp, _i32]
-    L.fp8_gemm.argtypes = [_vp, _vp, _vp, _u32, _u32, _vp, _vp, _u32, _vp, _i32]
+    L.fp8_gemm_workspace_size.argtypes = [_u32, _u32, _u32, _i32, ctypes.POINTER(ctypes.c_size_t)]
+    L.fp8_gemm.argtypes = [_vp, _vp, _vp, _u32, _u32, _vp, _vp, _u32, _vp, _i32, _vp, ctypes.c_size_t]
     L.rms_norm.argtypes = [_vp, ctypes.POINTER(Norm)]
     L.rotary_apply.argtypes = [_vp, ctypes.POINTER(Rotary)]
     L.ecw_last_error.restype = ctypes.c_char_p

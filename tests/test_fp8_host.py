@@ -1,6 +1,7 @@
 """Refusals of the 8-bit, norm and rotary entry points, through the C ABI and without a GPU: a
 bad call returns its status before anything is launched.  And the oracle's own format, and
 the frequencies as fractions of a turn."""
+import ctypes
 import math
 from fractions import Fraction
 
@@ -13,7 +14,7 @@ from entropy_coded_weight_amd import fp8
 from tests import fp8_abi as A
 from tests import fp8_ref as R
 
-OK, INVALID, UNSUPPORTED = 0, 1, 2
+OK, INVALID, UNSUPPORTED, TOO_SMALL = 0, 1, 2, 4
 P = 1 << 20  # an aligned address that nothing reads
 
 
@@ -57,12 +58,32 @@ def test_quantize_and_dequantize(L, change, status):
     ({"batch": 0}, OK), ({"rows": 0}, OK), ({"cols": 0}, INVALID), ({"w": P + 8}, INVALID), ({"ws": 0}, INVALID),
     ({"x": 0}, INVALID), ({"xs": P + 1}, INVALID), ({"y": 0}, INVALID), ({"y": P + 8}, INVALID),
     ({"yd": ecw.DT_FP8_E4M3}, INVALID), ({"batch": 1 << 25}, INVALID), ({"rows": 1 << 31}, INVALID),
-    ({"rows": 1 << 30, "batch": 1 << 20, "cols": 64}, UNSUPPORTED)])
+    ({"rows": 1 << 30, "batch": 1 << 20, "cols": 64}, UNSUPPORTED),
+    ({"batch": 40, "rows": 64, "cols": 16384, "workspace": 0}, INVALID),
+    ({"batch": 40, "rows": 64, "cols": 16384, "workspace": P + 8}, INVALID),
+    ({"batch": 40, "rows": 64, "cols": 16384, "bytes": 40 * 64 * 4}, TOO_SMALL)])
 def test_gemm(L, change, status):
-    a = {"w": P, "ws": P, "rows": 16, "cols": 64, "x": P, "xs": P, "batch": 2, "y": P, "yd": ecw.DT_F32, **change}
-    assert L.fp8_gemm(None, a["w"], a["ws"], a["rows"], a["cols"], a["x"], a["xs"], a["batch"], a["y"], a["yd"]) == status
+    a = {"w": P, "ws": P, "rows": 16, "cols": 64, "x": P, "xs": P, "batch": 2, "y": P, "yd": ecw.DT_F32, "workspace": P,
+         "bytes": 1 << 40, **change}
+    assert L.fp8_gemm(None, a["w"], a["ws"], a["rows"], a["cols"], a["x"], a["xs"], a["batch"], a["y"], a["yd"],
+                      a["workspace"], a["bytes"]) == status
     if status:
         assert L.ecw_last_error()
+
+
+def test_gemm_workspace(L):
+    """Parts of the columns for a few tiles only, a whole number of fp32 results each, and never
+    more of them than CUs."""
+    n = ctypes.c_size_t(7)
+    for rows, cols, batch, yd in [(0, 64, 4, 1), (64, 64, 0, 1), (64, 4096, 1, 2), (4096, 4096, 4096, 2), (64, 128, 40, 3)]:
+        assert L.fp8_gemm_workspace_size(rows, cols, batch, yd, n) == OK and n.value == 0
+    for rows, cols, batch, yd in [(64, 16384, 40, 3), (63, 14336, 33, 2), (4096, 14336, 40, 3), (1000, 30000, 100, 1)]:
+        assert L.fp8_gemm_workspace_size(rows, cols, batch, yd, n) == OK
+        part = -(-rows * batch // 4) * 16
+        assert n.value % part == 0 and 2 <= n.value // part <= 256
+    for rows, cols, batch, yd in [(64, 0, 4, 1), (1 << 31, 64, 4, 1), (64, 64, 1 << 25, 1), (64, 64, 4, ecw.DT_I8)]:
+        assert L.fp8_gemm_workspace_size(rows, cols, batch, yd, n) == INVALID
+    assert L.fp8_gemm_workspace_size(64, 64, 4, 1, None) == INVALID
 
 
 @pytest.mark.parametrize("change,status", [

@@ -171,6 +171,19 @@ def test_product_of_whole_numbers_is_exact(batch, rows, cols):
         assert torch.equal(wt.gemm(xt, out_dtype=dtype).cpu(), want.to(dtype))
 
 
+@pytest.mark.parametrize("batch,rows,cols", [(2048, 9000, 256), (4096, 4700, 130), (300, 14336, 512), (1500, 3001, 640), (17, 20000, 257),
+                                             (16, 16, 30000), (4, 300, 20000), (40, 100, 25000)])
+@pytest.mark.parametrize("out", DTYPES)
+def test_large_products_of_whole_numbers_are_exact(batch, rows, cols, out):
+    """Tiles of every kind, rounds that are cut, columns in parts; the reference, fp32 sums of
+    the same whole numbers under 2^24, is exact on the GPU too."""
+    most = 3 if cols < 10000 else 1
+    x, w = _whole(batch, cols, most, 1, 1).cuda(), _whole(rows, cols, most, 2, 1).cuda()
+    want = x @ w.t()
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(ecw.fp8_quantize(w).gemm(ecw.fp8_quantize(x), out_dtype=out), want.to(out))
+
+
 @pytest.mark.parametrize("batch,rows,cols", [(1, 1024, 4096), (6, 333, 14336), (40, 256, 5000), (130, 200, 2000), (513, 700, 1500)])
 @pytest.mark.parametrize("out", DTYPES)
 def test_product_of_real_numbers(batch, rows, cols, out):
