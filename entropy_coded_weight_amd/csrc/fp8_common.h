@@ -59,7 +59,7 @@ __device__ __forceinline__ u32x2 fp8_oct(const float (&v)[8], uint32_t* byte) {
   const float s = scale_of(254 - b);  // 2^-s
   float u[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = fminf(fmaxf(v[i] * s, -kFp8Top), kFp8Top);
+  for (int i = 0; i < 8; ++i) u[i] = __builtin_amdgcn_fmed3f(v[i] * s, -kFp8Top, kFp8Top);
   int lo = 0, hi = 0;
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], lo, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], lo, true);
@@ -140,7 +140,17 @@ __device__ __forceinline__ auto load_oct(const void* from, uint32_t c, uint32_t 
   }
 }
 // The same of a row of at least 8 columns, by one load that no branch is in the way of: from
-// column min(c, cols - 8), moved down by what is too much.
+// column min(c, cols - 8), and moved down by what is too much once it is there.
+template <int DT>
+__device__ __forceinline__ auto load_within(const void* row, uint32_t c, uint32_t cols) {
+  const uint32_t at = min(c, cols - 8);
+  if constexpr (DT == ECW_DT_F32) {
+    const float* from = static_cast<const float*>(row) + at;
+    return Oct32{reinterpret_cast<const Loose32*>(from)->v, reinterpret_cast<const Loose32*>(from + 4)->v};
+  } else {
+    return Oct16{reinterpret_cast<const Loose16*>(static_cast<const uint16_t*>(row) + at)->v};
+  }
+}
 __device__ __forceinline__ Oct16 moved_down(const Oct16& x, uint32_t by) {
   const unsigned __int128 t = __builtin_bit_cast(unsigned __int128, x.v);
   return {__builtin_bit_cast(u32x4, by < 8 ? t >> (16 * by) : (unsigned __int128)0)};
@@ -152,20 +162,6 @@ __device__ __forceinline__ Oct32 moved_down(const Oct32& x, uint32_t by) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = min(by, 8u) & k ? v[i + k] : v[i];
   return {{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}};
-}
-template <int DT>
-__device__ __forceinline__ auto load_within(const void* row, uint32_t c, uint32_t cols) {
-  const uint32_t at = min(c, cols - 8);
-  if constexpr (DT == ECW_DT_F32) {
-    const float* from = static_cast<const float*>(row) + at;
-    Oct32 r{reinterpret_cast<const Loose32*>(from)->v, reinterpret_cast<const Loose32*>(from + 4)->v};
-    if (at != c) r = moved_down(r, c - at);
-    return r;
-  } else {
-    Oct16 r{reinterpret_cast<const Loose16*>(static_cast<const uint16_t*>(row) + at)->v};
-    if (at != c) r = moved_down(r, c - at);
-    return r;
-  }
 }
 template <int DT>
 __device__ __forceinline__ void widen(float (&v)[8], const Oct16& x) {

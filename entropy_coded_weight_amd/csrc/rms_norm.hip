@@ -3,9 +3,14 @@
 //
 // A row is held in registers between the sum of its squares and its output, so x and the
 // residual are read once: LANES lanes hold it, 8 neighbouring columns at a time, OCTS times.
-// h stays in fp32 and is rounded once, into the new residual; y is made of the unrounded h,
-// in fp32, and rounded once.  The sum of squares is fp32: up to 32 products a lane in order,
-// then a tree.  Bound by memory; for a few rows by the latency of a load, the sum and a store.
+// h stays in fp32 and is rounded once, into the new residual; y is made of the unrounded h.
+// The sum of squares is fp32: up to 32 products a lane in order, then a tree.  The factor and
+// the products carry what their rounding lost along, so that y is rounded about once in fp32:
+// next to the memory that costs nothing, and fewer numbers come to lie on the other side of
+// an 8-bit border.  A group of lanes takes rows in turn and asks for the next one before it
+// sums up the last.  Bound by memory (8191 rows of 4096 bf16 with a bf16 residual into 8 bits
+// 39.8 us, 5.9 TB/s, with an fp32 one 71.0, 5.2); for a few rows by the latency of a load, the
+// sum and a store (one row 3.6 us).
 #include <type_traits>
 
 #include "fp8_common.h"
@@ -22,13 +27,21 @@ struct NormArgs {
   float eps, mean;            // mean: 1 / cols
 };
 
-// Eight columns of a row as fp32.  SMALL: rows may have less than eight.
+// Eight columns of a row from column c on, as they lie (moved, see load_within) and as fp32.
+// SMALL: rows may have less than eight.
+template <int DT, bool SMALL>
+__device__ __forceinline__ auto ask_oct(const void* row, uint32_t c, uint32_t cols) {
+  if (SMALL && cols < 8) return load_oct<DT>(row, c, cols);
+  return load_within<DT>(row, c, cols);
+}
+template <int DT, class T>
+__device__ __forceinline__ void have_oct(float (&v)[8], T raw, uint32_t c, uint32_t cols) {
+  if (c + 8 > cols && cols >= 8) raw = moved_down(raw, c - (cols - 8));
+  widen<DT>(v, raw);
+}
 template <int DT, bool SMALL>
 __device__ __forceinline__ void read_oct(float (&v)[8], const void* row, uint32_t c, uint32_t cols) {
-  if (SMALL && cols < 8)
-    widen<DT>(v, load_oct<DT>(row, c, cols));
-  else
-    widen<DT>(v, load_within<DT>(row, c, cols));
+  have_oct<DT>(v, ask_oct<DT, SMALL>(row, c, cols), c, cols);
 }
 template <bool SMALL>
 __device__ __forceinline__ void weight_oct(float (&w)[8], const NormArgs& a, uint32_t c) {
@@ -47,6 +60,13 @@ __device__ __forceinline__ void weight_oct(float (&w)[8], const NormArgs& a, uin
 // The sum over a row's LANES lanes, in every one of them.  `turn`: alternates between calls.
 template <int LANES>
 __device__ __forceinline__ float row_sum(float s, float (&sums)[2][16], uint32_t turn) {
+  if constexpr (LANES == 8) {
+    auto add = [&](auto step) { s += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(s), decltype(step)::value, 0xf, 0xf, false)); };
+    add(std::integral_constant<int, 0x141>{});  // lanes the other way round within 8
+    add(std::integral_constant<int, 0xb1>{});   // neighbours
+    add(std::integral_constant<int, 0x4e>{});   // pairs of a quad
+    return s;
+  }
   s = sum16(s);
   if constexpr (LANES >= 64) {
     s += __shfl_xor(s, 16);
@@ -68,39 +88,89 @@ template <int DX, int DR, int LANES, int OCTS>
 __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs a) {
   constexpr uint32_t kBlock = LANES < 256 ? 256 : LANES, kRows = kBlock / LANES;
   constexpr int kX = DX == ECW_DT_F32 ? 4 : 2, kR = DR == ECW_DT_F32 ? 4 : 2;
-  constexpr bool kSmall = LANES == 16;
+  constexpr bool kSmall = LANES <= 16;
+  constexpr bool kHold = OCTS <= 2;  // registers for the weight, and for the next row
   __shared__ float sums[2][16];
   const uint32_t lane = threadIdx.x % LANES;
+  using X = std::conditional_t<DX == ECW_DT_F32, Oct32, Oct16>;
+  using R = std::conditional_t<DR == ECW_DT_F32, Oct32, Oct16>;
+  struct Row {
+    X x[OCTS];
+    R r[DR ? OCTS : 1];
+  };
+  // rows past the last are computed as the last, so that every lane takes as many turns
+  auto row_of = [&](uint32_t first) { return min(first + threadIdx.x / LANES, a.rows - 1); };
+  auto ask = [&](Row& to, uint32_t first) {
+    const uint32_t row = row_of(first);
+#pragma unroll
+    for (int j = 0; j < OCTS; ++j) {
+      const uint32_t c = (lane + j * LANES) * 8;
+      to.x[j] = ask_oct<DX, kSmall>(static_cast<const uint8_t*>(a.x) + row * a.x_stride * kX, c, a.cols);
+      if constexpr (DR != 0)
+        to.r[j] = ask_oct<DR, kSmall>(static_cast<const uint8_t*>(a.residual) + row * a.residual_stride * kR, c, a.cols);
+    }
+  };
+  Row raw;
+  ask(raw, blockIdx.x * kRows);
+  float w[kHold ? OCTS : 1][8];
+  if constexpr (kHold) {
+#pragma unroll
+    for (int j = 0; j < OCTS; ++j) weight_oct<kSmall>(w[j], a, (lane + j * LANES) * 8);
+  }
+  // whether one of the lane's weights is infinite, which what was lost must not be multiplied by
+  bool infinite = false;
+  auto look = [&](const float (&of)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) infinite |= fabsf(of[i]) == INFINITY;
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int j = 0; j < OCTS; ++j) look(w[j]);
+  }
   uint32_t turn = 0;
-  // every lane of a block takes as many turns: rows past the last are computed as the last
   for (uint32_t first = blockIdx.x * kRows; first < a.rows; first += gridDim.x * kRows, turn ^= 1) {
     const bool real = first + threadIdx.x / LANES < a.rows;
-    const uint32_t row = real ? first + threadIdx.x / LANES : a.rows - 1;
+    const uint32_t row = row_of(first);
     float h[OCTS][8];
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < OCTS; ++j) {
-      const uint32_t oct = lane + j * LANES;
-      read_oct<DX, kSmall>(h[j], static_cast<const uint8_t*>(a.x) + row * a.x_stride * kX, oct * 8, a.cols);
+      const uint32_t c = (lane + j * LANES) * 8;
+      have_oct<DX>(h[j], raw.x[j], c, a.cols);
       if constexpr (DR != 0) {
         float r[8];
-        read_oct<DR, kSmall>(r, static_cast<const uint8_t*>(a.residual) + row * a.residual_stride * kR, oct * 8, a.cols);
+        have_oct<DR>(r, raw.r[j], c, a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[j][i] += r[i];
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fmaf(h[j][i], h[j][i], sum);
     }
-    const float f = 1.f / sqrtf(row_sum<LANES>(sum, sums, turn) * a.mean + a.eps);
+    if constexpr (kHold) ask(raw, first + gridDim.x * kRows);
+    const float m = row_sum<LANES>(sum, sums, turn) * a.mean + a.eps;
+    const bool tiny = m < 0x1p-96f;  // the instruction takes no subnormal numbers
+    const float f = __builtin_amdgcn_rsqf(tiny ? m * 0x1p96f : m) * (tiny ? 0x1p48f : 1.f);
+    // f + g is 1 / sqrt(m) to twice the precision: one step of Newton, its products exact (where
+    // f is no ordinary number there is nothing to add)
+    const float p = m * f, g0 = 0.5f * f * (fmaf(-p, f, 1.f) - fmaf(m, f, -p) * f), g = g0 - g0 == 0.f ? g0 : 0.f;
 #pragma unroll
     for (int j = 0; j < OCTS; ++j) {
       const uint32_t oct = lane + j * LANES, c = oct * 8, n = a.cols > c ? a.cols - c : 0;
       if constexpr (DR != 0)
         if (real) store_values<DR>(static_cast<uint8_t*>(a.residual_out) + row * a.residual_out_stride * kR, c, h[j], n);
-      float w[8], v[8];
-      weight_oct<kSmall>(w, a, c);
+      float (&wj)[8] = w[kHold ? j : 0];
+      if constexpr (!kHold) {
+        weight_oct<kSmall>(wj, a, c);
+        infinite = false;
+        look(wj);
+      }
+      float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = h[j][i] * f * w[i];
+      for (int i = 0; i < 8; ++i) {
+        const float hf = h[j][i] * f, lost = fmaf(h[j][i], g, fmaf(h[j][i], f, -hf));
+        v[i] = fmaf(hf, wj[i], lost * wj[i]);
+        if (infinite) v[i] = hf * wj[i];
+      }
       const uint64_t at = (uint64_t)row * a.cols + c;
       if (a.y_dtype == 0) {
         uint32_t b;
@@ -115,6 +185,8 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs
           store_values<ECW_DT_F32>(a.y, at, v, n);
       }
     }
+    if constexpr (!kHold)
+      if (first + gridDim.x * kRows < a.rows) ask(raw, first + gridDim.x * kRows);
   }
 }
 
@@ -134,11 +206,17 @@ ecw_status launch_norm(hipStream_t stream, const NormArgs& a) {
   return launched("rms_norm");
 }
 
+// Lanes of a row by its length.  Rows within a wave need no barrier (20000 rows of 1000 bf16
+// columns with a residual into 8 bits 26.5 us in a wave of 2 octets a lane, 36.0 in blocks of
+// 256 lanes), but 4 octets a lane are fewer rows in flight (8000 rows of 2048 18.4, in blocks
+// 15.4).  300000 rows of 64 13.5 us by 8 lanes, 25.7 by 16.
 template <int DX, int DR>
 ecw_status launch_norm(hipStream_t stream, const NormArgs& a) {
   const uint32_t octs = (a.cols + 7) / 8;
+  if (octs <= 8 && a.y_dtype != 0) return launch_norm<DX, DR, 8, 1>(stream, a);  // 8-bit blocks are 16 lanes
   if (octs <= 16) return launch_norm<DX, DR, 16, 1>(stream, a);
   if (octs <= 64) return launch_norm<DX, DR, 64, 1>(stream, a);
+  if (octs <= 128) return launch_norm<DX, DR, 64, 2>(stream, a);
   if (octs <= 256) return launch_norm<DX, DR, 256, 1>(stream, a);
   if (octs <= 512) return launch_norm<DX, DR, 256, 2>(stream, a);
   if (octs <= 1024) return launch_norm<DX, DR, 256, 4>(stream, a);

@@ -9,8 +9,11 @@
 // turn to either side of a quarter, go through the Taylor series of sine and cosine (the
 // first term left out is under 2^-29 and 2^-31).
 //
-// A lane holds 8 pairs of a row and turns them in `heads` heads of q and k, one after the
-// other, with one set of sines.  Bound by memory; for a few rows by latency.
+// A lane holds 8 pairs of a row and turns them in some heads of q and k, one after the other
+// with one set of sines, the next head asked for before one is stored.  Neighbouring lanes
+// have neighbouring heads.  Bound by memory (8191 rows of 40 heads of 128 in bf16 on three axes
+// 39.4 us, 4.3 TB/s, in place 34.3); for a few rows by latency (8 rows 3.8 us: positions,
+// then sines, with the first head's load next to them).
 #include <type_traits>
 
 #include "fp8_common.h"
@@ -26,7 +29,7 @@ struct RotaryArgs {
   int64_t q_row, q_head, k_row, k_head, qo_row, qo_head, ko_row, ko_head, axis_stride;
   uint32_t rows, q_heads, heads, dim, pairs, n_axes;  // heads: of q and k together
   uint32_t lanes;       // of a row and head: 8 pairs each, then 16 dimensions that are only copied
-  uint32_t each, parts; // heads of a lane; lanes along a row's heads
+  uint32_t parts;       // lanes along a row's heads: part p has heads p, p + parts, ...
   uint32_t wide;        // positions of 64 bits
   uint32_t copy;        // dimensions past the pairs are copied
   float scale;
@@ -51,15 +54,15 @@ __device__ __forceinline__ void cos_sin(uint32_t turn, float* c, float* s) {
   *s = quarter & 2 ? -r : r;
 }
 
-// NEAR: a pair is two neighbouring dimensions; else dimension j and j + pairs.
-template <int DT, bool NEAR>
+// NEAR: a pair is two neighbouring dimensions; else dimension j and j + pairs.  WHOLE: every
+// lane has all of its 16 dimensions.
+template <int DT, bool NEAR, bool WHOLE>
 __global__ void __launch_bounds__(256) k_rotary(RotaryArgs a) {
   constexpr int kSize = DT == ECW_DT_F32 ? 4 : 2;
   const uint32_t at = blockIdx.x * 256 + threadIdx.x;  // the host keeps the launch under 2^32 lanes
   const uint32_t group = at / a.lanes, lane = at - group * a.lanes;
   const uint32_t row = group / a.parts, part = group - row * a.parts;
   if (row >= a.rows) return;
-  const uint32_t first = part * a.each, end = min(first + a.each, a.heads);
   const uint32_t turned = (a.pairs + 7) / 8;
   auto from = [&](uint32_t head) {
     return head < a.q_heads ? static_cast<const uint8_t*>(a.q) + (row * a.q_row + head * a.q_head) * kSize
@@ -69,57 +72,66 @@ __global__ void __launch_bounds__(256) k_rotary(RotaryArgs a) {
     return head < a.q_heads ? static_cast<uint8_t*>(a.q_out) + (row * a.qo_row + head * a.qo_head) * kSize
                             : static_cast<uint8_t*>(a.k_out) + (row * a.ko_row + (head - a.q_heads) * a.ko_head) * kSize;
   };
-  if (lane >= turned) {  // 16 dimensions that are not turned
-    const uint32_t d = 2 * a.pairs + (lane - turned) * 16;
-    for (uint32_t head = first; head < end; ++head) {
-      float u[8], v[8];
-      widen<DT>(u, load_oct<DT>(from(head), d, a.dim));
-      widen<DT>(v, load_oct<DT>(from(head), d + 8, a.dim));
-      store_values<DT>(to(head), d, u, a.dim - d);
-      if (d + 8 < a.dim) store_values<DT>(to(head), d + 8, v, a.dim - d - 8);
-    }
-    return;
+  // two octets of dimensions of a head: where they start, and how much of each there is
+  uint32_t d0, d1, n0, n1;
+  const bool turns = lane < turned;
+  const uint32_t j0 = lane * 8;
+  if (!turns) {  // 16 dimensions that are only copied
+    d0 = 2 * a.pairs + (lane - turned) * 16, d1 = d0 + 8;
+    n0 = min(a.dim - d0, 8u), n1 = a.dim > d1 ? min(a.dim - d1, 8u) : 0;
+  } else if (NEAR) {
+    d0 = 2 * j0, d1 = d0 + 8;
+    n0 = min(2 * a.pairs - d0, 8u), n1 = 2 * a.pairs > d1 ? min(2 * a.pairs - d1, 8u) : 0;
+  } else {
+    d0 = j0, d1 = a.pairs + j0;
+    n0 = n1 = min(a.pairs - j0, 8u);
   }
-  const uint32_t j0 = lane * 8, n = min(a.pairs - j0, 8u);
-  float c[8], s[8];
-#pragma unroll
-  for (uint32_t i = 0; i < 8; ++i) {
-    const uint32_t j = min(j0 + i, a.pairs - 1);
-    const int64_t p = min((uint32_t)a.axes[j], a.n_axes - 1) * a.axis_stride + row;
-    const int64_t position = a.wide ? static_cast<const int64_t*>(a.positions)[p] : static_cast<const int32_t*>(a.positions)[p];
-    cos_sin((uint32_t)(((uint64_t)position * a.freqs[j] + (1ull << 31)) >> 32), &c[i], &s[i]);
-    c[i] *= a.scale;
-    s[i] *= a.scale;
-  }
-  for (uint32_t head = first; head < end; ++head) {
+  using Oct = std::conditional_t<DT == ECW_DT_F32, Oct32, Oct16>;
+  Oct u, v;
+  auto ask = [&](uint32_t head) {
     const uint8_t* x = from(head);
-    uint8_t* y = to(head);
-    float u[8], v[8];
-    if constexpr (NEAR) {
-      widen<DT>(u, load_oct<DT>(x, 2 * j0, 2 * a.pairs));
-      widen<DT>(v, load_oct<DT>(x, 2 * j0 + 8, 2 * a.pairs));
+    u = load_oct<DT>(x, d0, WHOLE ? ~0u : d0 + n0);
+    v = load_oct<DT>(x, d1, WHOLE ? ~0u : d1 + n1);
+  };
+  ask(part);
+  float c[8], s[8];
+  if (turns) {
+    int64_t position = 0;
+    auto position_of = [&](uint32_t axis) {
+      const int64_t p = axis * a.axis_stride + row;
+      return a.wide ? static_cast<const int64_t*>(a.positions)[p] : (int64_t)static_cast<const int32_t*>(a.positions)[p];
+    };
+    if (a.n_axes == 1) position = position_of(0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = u[2 * i], o = u[2 * i + 1], f = v[2 * i], p = v[2 * i + 1];
-        u[2 * i] = fmaf(e, c[i], -(o * s[i]));
-        u[2 * i + 1] = fmaf(o, c[i], e * s[i]);
-        v[2 * i] = fmaf(f, c[4 + i], -(p * s[4 + i]));
-        v[2 * i + 1] = fmaf(p, c[4 + i], f * s[4 + i]);
-      }
-      store_values<DT>(y, 2 * j0, u, 2 * n);
-      if (n > 4) store_values<DT>(y, 2 * j0 + 8, v, 2 * n - 8);
-    } else {
-      widen<DT>(u, load_oct<DT>(x, j0, a.pairs));
-      widen<DT>(v, load_oct<DT>(x, a.pairs + j0, 2 * a.pairs));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = u[i], o = v[i];
-        u[i] = fmaf(e, c[i], -(o * s[i]));
-        v[i] = fmaf(o, c[i], e * s[i]);
-      }
-      store_values<DT>(y, j0, u, n);
-      store_values<DT>(y, a.pairs + j0, v, n);
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t j = WHOLE ? j0 + i : min(j0 + i, a.pairs - 1);
+      if (a.n_axes > 1) position = position_of(min((uint32_t)a.axes[j], a.n_axes - 1));
+      cos_sin((uint32_t)(((uint64_t)position * a.freqs[j] + (1ull << 31)) >> 32), &c[i], &s[i]);
+      c[i] *= a.scale;
+      s[i] *= a.scale;
     }
+  }
+  for (uint32_t head = part; head < a.heads; head += a.parts) {
+    float x[8], y[8];
+    widen<DT>(x, u);
+    widen<DT>(y, v);
+    if (head + a.parts < a.heads) ask(head + a.parts);
+    if (turns) {
+      auto turn = [&](float& e, float& o, int k) {
+        const float before = e;
+        e = fmaf(e, c[k], -(o * s[k]));
+        o = fmaf(o, c[k], before * s[k]);
+      };
+      if constexpr (NEAR) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) turn(x[2 * k], x[2 * k + 1], k), turn(y[2 * k], y[2 * k + 1], 4 + k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) turn(x[k], y[k], k);
+      }
+    }
+    store_values<DT>(to(head), d0, x, WHOLE ? 8 : n0);
+    if (WHOLE || n1) store_values<DT>(to(head), d1, y, WHOLE ? 8 : n1);
   }
 }
 
@@ -129,12 +141,20 @@ using namespace ecw;
 
 namespace {
 
+template <int DT, bool NEAR>
+void launch_rotary(hipStream_t stream, uint32_t grid, const RotaryArgs& a) {
+  const bool whole = a.pairs % 8 == 0 && (!a.copy || (a.dim - 2 * a.pairs) % 16 == 0);
+  if (whole)
+    hipLaunchKernelGGL((k_rotary<DT, NEAR, true>), dim3(grid), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_rotary<DT, NEAR, false>), dim3(grid), dim3(256), 0, stream, a);
+}
 template <int DT>
 void launch_rotary(hipStream_t stream, uint32_t grid, bool near, const RotaryArgs& a) {
   if (near)
-    hipLaunchKernelGGL((k_rotary<DT, true>), dim3(grid), dim3(256), 0, stream, a);
+    launch_rotary<DT, true>(stream, grid, a);
   else
-    hipLaunchKernelGGL((k_rotary<DT, false>), dim3(grid), dim3(256), 0, stream, a);
+    launch_rotary<DT, false>(stream, grid, a);
 }
 
 }  // namespace
@@ -166,14 +186,16 @@ extern "C" ecw_status rotary_apply(ecw_stream stream, const ecw_rotary* r) {
   RotaryArgs a{r->q, r->k, r->q_out, r->k_out, r->positions, static_cast<const uint64_t*>(r->freqs),
                static_cast<const uint8_t*>(r->axis_of), r->q_row, r->q_head, r->k_row, r->k_head, r->q_out_row,
                r->q_out_head, r->k_out_row, r->k_out_head, r->axis_stride, r->rows, r->q_heads, heads, r->head_dim,
-               r->rotary_dim / 2, r->axes, 0, 0, 0, r->wide_positions ? 1u : 0u, 0, r->scale};
+               r->rotary_dim / 2, r->axes, 0, 0, r->wide_positions ? 1u : 0u, 0, r->scale};
   const bool in_place = (!r->q_heads || r->q == r->q_out) && (!r->k_heads || r->k == r->k_out);
   a.copy = !in_place && r->rotary_dim < r->head_dim;
   a.lanes = (a.pairs + 7) / 8 + (a.copy ? (r->head_dim - r->rotary_dim + 15) / 16 : 0);
-  // several heads a lane once the card is full, for sines cost as much as a head or two
-  a.each = 1;
-  while (a.each < 8 && a.each < heads && (uint64_t)r->rows * a.lanes * ((heads + 2 * a.each - 1) / (2 * a.each)) >= 256 * 2048) a.each *= 2;
-  a.parts = (heads + a.each - 1) / a.each;
+  // up to eight heads a lane while there are lanes enough, for sines cost as much as a head or
+  // two (8191 rows of 40 heads of 128: 8 heads 39 us, 4 45, 16 44; 4000 rows of 40 heads of 64
+  // 12.2 us, with one head a lane 17.2)
+  uint32_t each = 1;
+  while (each < 8 && each < heads && (uint64_t)r->rows * a.lanes * ((heads + 2 * each - 1) / (2 * each)) >= 256 * 512) each *= 2;
+  a.parts = (heads + each - 1) / each;
   const uint64_t grid = ((uint64_t)r->rows * a.parts * a.lanes + 255) / 256;
   if (!launchable(grid, 256)) return refuse(ECW_E_UNSUPPORTED, "too many rows and heads for one launch");
   const auto s = (hipStream_t)stream;
