@@ -39,7 +39,7 @@ def _bind_flags():
     return (["-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
              "-D__HIP_PLATFORM_AMD__=1", f"-I{python}", f"-I{rocm}"]
             + [f"-isystem{p}" for p in include_paths()],
-            [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"])
+            [f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-ltorch_hip"])
 
 
 HIP_SOURCES = ("ecw_kernels.hip", "ecw_probes.hip", "mx4_quant.hip", "mx4_gemm.hip", "kv4.hip", "fp8_quant.hip",

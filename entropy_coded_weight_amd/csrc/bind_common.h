@@ -12,6 +12,7 @@
 #include <string>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 
 #include "../../include/ecw.h"
 
@@ -81,9 +82,14 @@ void written(const at::Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
+// A new tensor on like's device, from torch's allocator without a turn through its dispatcher.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+}
+
 // the given output, or a new one
 at::Tensor output(PyObject* o, const at::Tensor& like, at::IntArrayRef shape, at::ScalarType type, const char* name) {
-  if (o == Py_None) return at::empty(shape, like.options().dtype(type));
+  if (o == Py_None) return fresh(shape, type, like);
   const at::Tensor& t = tensor(o, name);
   if (t.sizes() != shape || !t.is_contiguous() || t.device() != like.device()) {
     std::string s;

@@ -95,7 +95,7 @@ PyObject* py_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     size_t bytes = 0;
     check(api.workspace((uint32_t)rows, (uint32_t)cols, batch, yd, &bytes), "fp8_gemm_workspace_size");
     at::Tensor ws;
-    if (bytes) ws = at::empty({(int64_t)bytes}, codes.options());
+    if (bytes) ws = fresh({(int64_t)bytes}, at::kByte, codes);
     check(api.gemm(stream_of(codes.device()), codes.data_ptr(), scales.data_ptr(), (uint32_t)rows, (uint32_t)cols,
                    xc.data_ptr(), xs.data_ptr(), batch, y.data_ptr(), yd, bytes ? ws.data_ptr() : nullptr, bytes),
           "fp8_gemm");
@@ -139,7 +139,7 @@ PyObject* py_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         bad_value("residual has shape " + shape_of(*residual) + ", x " + shape_of(x));
       p.residual = residual->data_ptr(), p.residual_stride = matrix(*residual, "residual", "[rows, cols]").stride;
       if (a[7] == Py_None) {
-        next = at::empty(x.sizes(), residual->options());
+        next = fresh(x.sizes(), residual->scalar_type(), x);
       } else {
         next = tensor(a[7], "residual_out");
         same_device(next, x, "residual_out", "input");
@@ -235,7 +235,7 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const c10::DeviceGuard guard(q.device());
     auto out_of = [&](PyObject* o, const at::Tensor& in, const char* name, const char* in_name) {
-      if (o == Py_None) return at::empty(in.sizes(), in.options());
+      if (o == Py_None) return fresh(in.sizes(), in.scalar_type(), in);
       const at::Tensor& t = tensor(o, name);
       same_device(t, q, name, "first");
       if (t.sizes() != in.sizes() || t.scalar_type() != in.scalar_type())

@@ -1,10 +1,12 @@
 """One transformer layer served in few bits: a prompt, then decode steps in one HIP graph.
 
 The attention projections are entropy-coded 4-bit weights (lossless for their codes), the
-feed-forward weights microscaled 4-bit floats, and keys and values live in a paged 4-bit
-cache.  Synthetic weights, no positional encoding.
+feed-forward weights microscaled 4-bit floats, or 8-bit ones next to 8-bit activations, and
+keys and values live in a paged 4-bit cache, with rotary positions if a base is given.
+Synthetic weights.
 
     python examples/decode_layer.py [--batch 4] [--prompt 512] [--steps 64] [--window 0]
+                                    [--feed mx4] [--rotary 0]
 """
 import argparse
 import os
@@ -40,8 +42,10 @@ class Pages:
 
 class Layer:
     def __init__(self, hidden=4096, heads=32, kv_heads=8, head_dim=128, inner=14336, batch=4, max_len=2048, window=0,
-                 sinks=4, seed=0):
+                 sinks=4, seed=0, feed="mx4", rotary=0.0):
         rng = np.random.default_rng(seed)
+        self.feed, self.inner = feed, inner
+        self.rotary = ecw.Rotary(head_dim, base=rotary) if rotary else None
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.window, self.sinks, self.max_len = window, sinks, max_len
 
@@ -52,11 +56,15 @@ class Layer:
 
         def micro(rows, cols):
             g = torch.Generator(device="cuda").manual_seed(int(rng.integers(1 << 30)))
-            return ecw.mx4_quantize((torch.randn(rows, cols, generator=g, device="cuda") / cols ** 0.5).to(torch.float16))
+            quantize = {"mx4": ecw.mx4_quantize, "fp8": ecw.fp8_quantize}[feed]
+            return quantize((torch.randn(rows, cols, generator=g, device="cuda") / cols ** 0.5).to(torch.float16))
 
         self.q, self.k, self.v = (coded(n * head_dim, hidden) for n in (heads, kv_heads, kv_heads))
         self.o = coded(hidden, heads * head_dim)
-        self.gate, self.up, self.down = micro(inner, hidden), micro(inner, hidden), micro(hidden, inner)
+        if feed == "fp8":  # gate and up in one matrix: one product, whose halves the down projection's input is made of
+            self.gate_up, self.down = micro(2 * inner, hidden), micro(hidden, inner)
+        else:
+            self.gate, self.up, self.down = micro(inner, hidden), micro(inner, hidden), micro(hidden, inner)
         self.pages = Pages(batch, max_len, 64)
         self.cache = ecw.KV4Cache(self.pages.count, kv_heads, head_dim)
 
@@ -64,14 +72,33 @@ class Layer:
     def norm(x):
         return (x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)).to(torch.float16)
 
-    def __call__(self, x, lens, starts=None):
-        """x fp32 [rows, hidden], the last rows of each sequence; lens with them."""
-        h = self.norm(x)
-        q, k, v = (w.gemm(h).to(torch.float16).view(x.shape[0], -1, self.head_dim) for w in (self.q, self.k, self.v))
+    def attention(self, h, lens, starts):
+        q, k, v = (w.gemm(h).to(torch.float16).view(h.shape[0], -1, self.head_dim) for w in (self.q, self.k, self.v))
+        if self.rotary:
+            q, k = self.rotary(q, k, self.positions(h.shape[0], lens, starts), out=(q, k))
         self.cache.append(k, v, self.pages.table, lens, starts)
         a = self.cache.attend(q, self.pages.table, lens, starts, max_len=self.max_len, window=self.window,
                               sinks=self.sinks)
-        x = x + self.o.gemm(a.view(x.shape[0], -1))
+        return self.o.gemm(a.view(h.shape[0], -1))
+
+    @staticmethod
+    def positions(rows, lens, starts):
+        """Where each row's token stands in its sequence: the rows are the sequences' last tokens."""
+        row = torch.arange(rows, dtype=torch.int32, device=lens.device)
+        if starts is None:
+            each = rows // lens.numel()
+            return (lens[:, None] - each + row[:each]).flatten()
+        b = torch.searchsorted(starts[1:].contiguous(), row, right=True).clamp_(max=lens.numel() - 1)
+        return lens[b] - starts[b + 1] + row
+
+    def __call__(self, x, lens, starts=None):
+        """x fp32 [rows, hidden], the last rows of each sequence; lens with them."""
+        if self.feed == "fp8":
+            y = self.attention(ecw.rms_norm(x, out_dtype=torch.float16), lens, starts)
+            h, x = ecw.rms_norm(y, residual=x, out_dtype=torch.float8_e4m3fn)
+            both = self.gate_up.gemm(h, out_dtype=torch.bfloat16)
+            return x + self.down.gemm(ecw.fp8_quantize(both[:, self.inner:], gate=both[:, :self.inner]))
+        x = x + self.attention(self.norm(x), lens, starts)
         h = self.norm(x)
         inner = torch.nn.functional.silu(self.gate.gemm(h)) * self.up.gemm(h)
         return x + self.down.gemm(inner.to(torch.float16))
@@ -104,8 +131,10 @@ def main():
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("batch", 4), ("prompt", 512), ("steps", 64), ("window", 0)):
         p.add_argument("--" + name, type=int, default=value)
+    p.add_argument("--feed", choices=("mx4", "fp8"), default="mx4")
+    p.add_argument("--rotary", type=float, default=0.0, help="base of the rotary positions, 0 for none")
     a = p.parse_args()
-    layer = Layer(batch=a.batch, max_len=a.prompt + a.steps, window=a.window)
+    layer = Layer(batch=a.batch, max_len=a.prompt + a.steps, window=a.window, feed=a.feed, rotary=a.rotary)
     x = torch.randn(a.batch, a.prompt, 4096, device="cuda")
     generate(layer, x, 2)
     begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
