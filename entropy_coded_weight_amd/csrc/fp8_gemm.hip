@@ -189,14 +189,15 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_fp8_gemm_few(Fp8GemmArgs a, 
 // there are few tiles the columns are cut too: blockIdx.y has `chunk` spans (a multiple of
 // KG), and k_fp8_gemm_join adds the parts up.
 //
-// The large tiles by the 8-bit instruction are bound by the copies: 8192 x 8192 x 8192 takes
-// 443 us (2.5 PFLOP/s), without reading or multiplying what was copied 360, with the matrix
-// instructions alone 297, where 8-bit numbers of a model draw more power than the card's
-// clock holds.  Reads of LDS that run one tile ahead of the instructions, the sums in
-// accumulation registers, gained 3%, waves that take turns at reading and multiplying lost 30%,
-// and words of later spans asked for ahead, to have them in L2, lost 5%: not kept.  By the
-// bf16 instruction the same takes 830 us (1.3 PFLOP/s; a bf16 library product of this size
-// runs at 1.38).
+// The large tiles by the 8-bit instruction are bound by the copies next to the matrix
+// instructions: 8192 x 8192 x 8192 takes 443 us (2.5 PFLOP/s), the matrix instructions alone
+// 297, they and the copies without a read of LDS 408, they and the reads without the copies
+// 326.  Copies alone run at 85 to 105 KB a us and CU, next to the instructions at 40 to 60.
+// Reads of LDS that run ahead of the instructions, the sums in accumulation registers, gained
+// 3%, waves that take turns at reading and multiplying lost 30%, words of later spans asked
+// for ahead, to have them in L2, lost 5%, operands of a whole span read ahead gained nothing
+// in any tile: not kept.  By the bf16 instruction the same takes 830 us (1.3 PFLOP/s; a bf16
+// library product of this size runs at 1.38).
 template <int WM, int WN, int TM, int TN, int NS, int KG>
 struct Fp8Tiles {
   static constexpr int kWaves = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
@@ -356,14 +357,21 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) k_fp8_gemm_tile(Fp8GemmArgs
   });
 }
 
-// The parts of the columns added up, in order, 4 outputs a lane.
+// The parts of the columns added up, in order, 4 outputs a lane, 4 parts asked for at once.
 template <int DT>
 __global__ void __launch_bounds__(256) k_fp8_gemm_join(const float* __restrict__ part, void* __restrict__ y, uint64_t all,
                                                        uint64_t part_size, uint32_t splits) {
   const uint64_t at = ((uint64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (at >= all) return;
-  f32x4 sum = *reinterpret_cast<const f32x4*>(part + at);
-  for (uint32_t s = 1; s < splits; ++s) sum += *reinterpret_cast<const f32x4*>(part + s * part_size + at);
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (uint32_t s = 0; s < splits; s += 4) {
+    f32x4 p[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const f32x4*>(part + min(s + i, splits - 1) * part_size + at);
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      if (s + i < splits) sum += p[i];
+  }
   const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
   store_run<DT>(y, at, v, (uint32_t)min(all - at, (uint64_t)4), true);
 }

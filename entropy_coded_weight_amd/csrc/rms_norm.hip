@@ -4,7 +4,8 @@
 // A row is held in registers between the sum of its squares and its output, so x and the
 // residual are read once: LANES lanes hold it, 8 neighbouring columns at a time, OCTS times.
 // h stays in fp32 and is rounded once, into the new residual; y is made of the unrounded h.
-// The sum of squares is fp32: up to 32 products a lane in order, then a tree.  The factor and
+// The sum of squares is fp32: up to 32 products a lane in order, then a tree; numbers are
+// multiplied by a power of two first, so that it stays in range as long as the mean does.  The factor and
 // the products carry what their rounding lost along, so that y is rounded about once in fp32:
 // next to the memory that costs nothing, and fewer numbers come to lie on the other side of
 // an 8-bit border.  A group of lanes takes rows in turn and asks for the next one before it
@@ -24,7 +25,8 @@ struct NormArgs {
   int64_t x_stride, residual_stride, residual_out_stride;
   uint32_t rows, cols, octs, scale_row;
   int weight_dtype, y_dtype;  // weight_dtype 0: none; y_dtype 0: 8 bits
-  float eps, mean;            // mean: 1 / cols
+  float eps;
+  float shrink, mean;         // a power of two, about 1 / sqrt(cols); 1 / cols without its square
 };
 
 // Eight columns of a row from column c on, as they lie (moved, see load_within) and as fp32.
@@ -144,7 +146,10 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs
         for (int i = 0; i < 8; ++i) h[j][i] += r[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(h[j][i], h[j][i], sum);
+      for (int i = 0; i < 8; ++i) {
+        const float u = h[j][i] * a.shrink;
+        sum = fmaf(u, u, sum);
+      }
     }
     if constexpr (kHold) ask(raw, first + gridDim.x * kRows);
     const float m = row_sum<LANES>(sum, sums, turn) * a.mean + a.eps;
@@ -251,10 +256,13 @@ extern "C" ecw_status rms_norm(ecw_stream stream, const ecw_rms_norm* n) {
     return refuse(ECW_E_INVALID_ARG, "residual and residual_out must be aligned device pointers");
   if (n->x_stride < 0 || (n->residual && (n->residual_stride < 0 || n->residual_out_stride < n->cols)))
     return refuse(ECW_E_INVALID_ARG, "row strides must not be negative, residual_out's at least cols");
+  float shrink = 1.f;
+  while (shrink * shrink * (float)n->cols > 1.f) shrink *= 0.5f;
   const NormArgs a{n->x, n->residual, n->weight, n->residual_out, n->y, static_cast<uint8_t*>(n->y_scales),
                    n->x_stride, n->residual_stride, n->residual_out_stride,
                    n->rows, n->cols, fp8_row(n->cols) / 8, fp8_scale_row(n->cols),
-                   n->weight ? n->weight_dtype : 0, eight ? 0 : n->y_dtype, n->eps, 1.f / (float)n->cols};
+                   n->weight ? n->weight_dtype : 0, eight ? 0 : n->y_dtype, n->eps, shrink,
+                   1.f / ((float)n->cols * shrink * shrink)};
   const auto s = (hipStream_t)stream;
   const int dr = n->residual ? n->residual_dtype : 0;
   if (n->x_dtype == ECW_DT_F32) return dr ? launch_norm<ECW_DT_F32, ECW_DT_F32>(s, a) : launch_norm<ECW_DT_F32, 0>(s, a);

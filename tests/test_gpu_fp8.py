@@ -172,7 +172,8 @@ def test_product_of_whole_numbers_is_exact(batch, rows, cols):
 
 
 @pytest.mark.parametrize("batch,rows,cols", [(2048, 9000, 256), (4096, 4700, 130), (300, 14336, 512), (1500, 3001, 640), (17, 20000, 257),
-                                             (16, 16, 30000), (4, 300, 20000), (40, 100, 25000)])
+                                             (16, 16, 30000), (4, 300, 20000), (40, 100, 25000), (33, 63, 20000), (19, 1, 9000),
+                                             (70, 2, 30000), (1, 3, 20001), (130, 130, 16385)])
 @pytest.mark.parametrize("out", DTYPES)
 def test_large_products_of_whole_numbers_are_exact(batch, rows, cols, out):
     """Tiles of every kind, rounds that are cut, columns in parts; the reference, fp32 sums of
@@ -302,3 +303,65 @@ def test_streams_and_graphs(batch):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_gate_and_operand_may_be_the_same_tensor():
+    x = _randn(5, 300, seed=1).cuda()
+    t = ecw.fp8_quantize(x, gate=x)
+    assert R.between(_f64(t.dequantize(torch.float32)), _f64(x) ** 2 / (1 + np.exp(-_f64(x))), 2.0 ** -21).all()
+    wide = _randn(5, 900, seed=2).cuda()  # a gate whose rows lie otherwise than x's
+    t = ecw.fp8_quantize(x, gate=wide[:, 3:303])
+    assert torch.equal(t.codes, ecw.fp8_quantize(x, gate=wide[:, 3:303].contiguous()).codes)
+    w = _whole(40, 300, 3, 1)
+    q = ecw.fp8_quantize(w.cuda())
+    assert torch.equal(q.gemm(q).cpu(), (w.double() @ w.double().t()).float())
+
+
+@pytest.mark.parametrize("batch", [3, 40, 300])
+def test_two_streams_and_two_graphs_at_once(batch):
+    """Calls that overlap share nothing: the same weights on two streams, and two graphs of them
+    replayed in turn."""
+    w = ecw.fp8_quantize(_whole(100, 20000, 1, 1).cuda())
+    xs = [ecw.fp8_quantize(_whole(batch, 20000, 1, 2 + i).cuda()) for i in range(2)]
+    want = [w.gemm(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(w.gemm(xs[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+    graphs, held = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            held.append(w.gemm(xs[i]))
+    for _ in range(3):
+        for y in held:
+            y.zero_()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                streams[i].wait_stream(torch.cuda.default_stream())
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(held[i], want[i]) for i in range(2))
+
+
+def test_offsets_past_32_bits():
+    """Rows that lie more than 2^32 bytes behind the first: as by themselves."""
+    rows, cols = 66000, 65536
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[:64], x[-64:] = _randn(64, cols, seed=1).cuda(), _randn(64, cols, seed=2).cuda()
+    t = ecw.fp8_quantize(x)
+    last = ecw.fp8_quantize(x[-64:])
+    assert torch.equal(t.codes[-64:], last.codes) and torch.equal(t.scales[-64:], last.scales)
+    assert torch.equal(t.dequantize(torch.bfloat16, out=x)[-64:], last.dequantize(torch.bfloat16))
+    del x
+    for batch in (1, 40, 200):
+        a = ecw.fp8_quantize(_randn(batch, cols, seed=3).cuda())
+        for out in (torch.float32, torch.bfloat16):
+            y, own = t.gemm(a, out_dtype=out)[:, -64:].float(), last.gemm(a, out_dtype=out).float()
+            # other tiles, so other orders of the same sums: 2^-12 of the largest, and a step of the output
+            assert (y - own).abs().max() <= (2.0 ** -12 + torch.finfo(out).eps) * own.abs().max()

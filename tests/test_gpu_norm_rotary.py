@@ -139,6 +139,40 @@ def test_norm_of_zeros_infinities_and_nan():
     assert torch.isfinite(t[[0, 1, 4, 5]]).all() and torch.isnan(t[3]).all() and torch.isnan(t[2, :128]).all() and (t[2, 128:] == 0).all()
 
 
+def test_norm_with_infinite_and_nan_weights():
+    """A weight that is infinite makes its column infinite, with the sign of its number; NaN its column NaN."""
+    x = _randn(3, 300, seed=1).abs() + 0.5
+    w = torch.ones(300, device="cuda")
+    w[7], w[8], w[200] = float("inf"), float("-inf"), float("nan")
+    y = ecw.rms_norm(x, w)
+    assert (y[:, 7] == float("inf")).all() and (y[:, 8] == float("-inf")).all() and torch.isnan(y[:, 200]).all()
+    rest = torch.ones(300, dtype=torch.bool)
+    rest[[7, 8, 200]] = False
+    assert torch.equal(y[:, rest], ecw.rms_norm(x)[:, rest])
+    t = ecw.rms_norm(x, w, out_dtype=EIGHT).dequantize(torch.float32)
+    assert torch.isnan(t[:, :256]).all() and torch.isfinite(t[:, 256:]).all()
+
+
+def test_norm_far_from_one():
+    """Numbers and factors near the ends of what squares in fp32 hold."""
+    x = _randn(4, 500, seed=1)
+    for size, eps in ((1e18, 1e-6), (1e-17, 0.0), (1e-18, 1e-38), (1.0, 1e30)):
+        _check_norm(x * size, None, None, eps, torch.float32)
+        _check_norm(x * size, None, x * size, eps, EIGHT)
+
+
+def test_norm_offsets_past_32_bits():
+    rows, cols = 132000, 32768
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = _randn(3, cols, seed=1).bfloat16()
+    y, h = ecw.rms_norm(x, residual=x)
+    want, wide = ecw.rms_norm(x[-3:], residual=x[-3:])
+    assert torch.equal(y[-3:], want) and torch.equal(h[-3:], wide)
+    del y, h
+    t, n = ecw.rms_norm(x, out_dtype=EIGHT), ecw.rms_norm(x[-3:], out_dtype=EIGHT)
+    assert torch.equal(t.codes[-3:], n.codes) and torch.equal(t.scales[-3:], n.scales)
+
+
 def test_norm_empty_and_refusals():
     x, w = torch.ones(4, 256, device="cuda"), torch.ones(256, device="cuda")
     assert ecw.rms_norm(x[:0], w).shape == (0, 256) and ecw.rms_norm(x[:0], out_dtype=EIGHT).shape == (0, 256)
@@ -273,6 +307,17 @@ def test_rotary_strides_and_in_place(dtype):
             assert torch.equal(y[:, :, dim:], want[0]) and (y[:, :, :dim] == 0).all()
     shared = qkv[:1, :dim].view(1, 1, dim).expand(rows, 3, dim)
     assert torch.equal(ecw.Rotary(dim)(shared, None, at), ecw.Rotary(dim)(shared.contiguous(), None, at))
+
+
+def test_rotary_offsets_past_32_bits():
+    rows, heads, dim = 270000, 128, 128
+    q = torch.empty(rows, heads, dim, dtype=torch.bfloat16, device="cuda")
+    q[-2:] = _randn(2, heads, dim, seed=1).bfloat16()
+    at = torch.arange(rows, dtype=torch.int32, device="cuda")
+    r = ecw.Rotary(dim)
+    want = r(q[-2:].clone(), None, at[-2:])
+    r(q, None, at, out=q)
+    assert torch.equal(q[-2:], want)
 
 
 def test_rotary_undone_by_negated_positions():
