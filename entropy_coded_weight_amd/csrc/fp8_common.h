@@ -84,9 +84,6 @@ __device__ __forceinline__ void store_fp8(uint8_t* codes, uint8_t* scales, uint3
 // Eight elements of a row of type DT from column c on, zeros from `cols` on.  What is left of
 // a row's last eight goes in pieces of 4, 2 and 1: of each, and no element by itself, so that
 // many of them in a kernel stay small.
-struct __attribute__((packed, aligned(2))) Loose8 {
-  u32x2 v;
-};
 struct __attribute__((packed, aligned(2))) Loose4 {
   uint32_t v;
 };

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) k_fp8_gemm_few(Fp8GemmArgs a, 
       if (r16 < a.batch && n < a.rows) {
         with_type(y_dtype, [&](auto dt) {
           const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-          store_run<dt.value>(a.y, (uint64_t)r16 * a.rows + n, v, a.rows - n, a.rows % 4 == 0);
+          store_run<dt.value>(a.y, (uint64_t)r16 * a.rows + n, v, a.rows - n);
         });
       }
     }
@@ -343,7 +343,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) k_fp8_gemm_tile(Fp8GemmArgs
   const uint32_t y_row = whole ? a.y_row : a.rows;
   if (!whole) y_dtype = ECW_DT_F32;
   with_type(y_dtype, [&](auto dt) {
-    const bool vec = y_row % (dt.value == ECW_DT_F32 ? 4 : 8) == 0;
 #pragma unroll
     for (int m = 0; m < TM; ++m) {
       const uint32_t b = m0 + (wm + m) * 16 + r16;
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) k_fp8_gemm_tile(Fp8GemmArgs
       for (int n = 0; n < TN; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[n * 4 + r] = acc[n][m][r];
-      if (b < a.batch) store_run<dt.value>(y, (uint64_t)b * y_row + at, v, a.rows - at, vec);
+      if (b < a.batch) store_run<dt.value>(y, (uint64_t)b * y_row + at, v, a.rows - at);
     }
   });
 }
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(256) k_fp8_gemm_join(const float* __restrict__
       if (s + i < splits) sum += p[i];
   }
   const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-  store_run<DT>(y, at, v, (uint32_t)min(all - at, (uint64_t)4), true);
+  store_run<DT>(y, at, v, (uint32_t)min(all - at, (uint64_t)4));
 }
 
 }  // namespace ecw

@@ -75,6 +75,9 @@ __device__ __forceinline__ void split_f16(u32x4 v, bf16x8* hi, bf16x8* lo) {
 struct __attribute__((packed, aligned(2))) Loose16 {
   u32x4 v;
 };
+struct __attribute__((packed, aligned(2))) Loose8 {
+  u32x2 v;
+};
 struct __attribute__((packed, aligned(4))) Loose32 {
   f32x4 v;
 };

@@ -580,7 +580,6 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) k_mx4_gemm_tile(GemmArgs a,
     if constexpr (T::kX4) {
       const uint32_t at = n0 + wn * 16 + g * (4 * TN);
       if (at >= a.rows) return;
-      const bool vec = a.rows % (dt.value == ECW_DT_F32 ? 4 : 8) == 0;
 #pragma unroll
       for (int m = 0; m < TM; ++m) {
         const uint32_t b = m0 + (wm + m) * 16 + r16;
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(64 * WM * WN * KG) k_mx4_gemm_tile(GemmArgs a,
         for (int n = 0; n < TN; ++n)
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[n * 4 + r] = acc[n][m][r];
-        if (b < a.batch) store_run<dt.value>(a.y, (uint64_t)b * a.rows + at, v, a.rows - at, vec);
+        if (b < a.batch) store_run<dt.value>(a.y, (uint64_t)b * a.rows + at, v, a.rows - at);
       }
     } else {
 #pragma unroll
