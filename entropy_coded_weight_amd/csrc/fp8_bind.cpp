@@ -29,10 +29,21 @@ void apart(const at::Tensor& out, const at::Tensor& in, const char* out_name, co
 struct Eight {
   at::Tensor codes, scales;
 };
-// the given codes and scales of a [rows, cols] matrix, or new ones
+// [rows, width] bytes of a tensor of bytes from `offset` on, with its storage
+at::Tensor bytes_of(const at::Tensor& all, int64_t offset, int64_t rows, int64_t width) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(offset);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({rows, width});
+  return t;
+}
+// the given codes and scales of a [rows, cols] matrix, or new ones, in one piece of memory
 Eight eight_bits(PyObject* codes, PyObject* scales, const at::Tensor& like, int64_t rows, int64_t cols) {
-  return {output(codes, like, {rows, (cols + 127) / 128 * 128}, at::kByte, "codes"),
-          output(scales, like, {rows, (cols + 2047) / 2048 * 16}, at::kByte, "scales")};
+  const int64_t wide = (cols + 127) / 128 * 128, scale_wide = (cols + 2047) / 2048 * 16;
+  if (codes == Py_None && scales == Py_None) {
+    const at::Tensor all = fresh({rows * (wide + scale_wide)}, at::kByte, like);
+    return {bytes_of(all, 0, rows, wide), bytes_of(all, rows * wide, rows, scale_wide)};
+  }
+  return {output(codes, like, {rows, wide}, at::kByte, "codes"), output(scales, like, {rows, scale_wide}, at::kByte, "scales")};
 }
 
 // quantize(x, gate or None, codes or None, scales or None) -> codes, scales, cols

@@ -365,3 +365,25 @@ def test_offsets_past_32_bits():
             y, own = t.gemm(a, out_dtype=out)[:, -64:].float(), last.gemm(a, out_dtype=out).float()
             # other tiles, so other orders of the same sums: 2^-12 of the largest, and a step of the output
             assert (y - own).abs().max() <= (2.0 ** -12 + torch.finfo(out).eps) * own.abs().max()
+
+
+def test_codes_and_scales_are_tensors_of_their_own():
+    """They share a piece of memory, and no byte of it; writing into them advances their versions."""
+    x = _randn(7, 300, seed=1).cuda()
+    t = ecw.fp8_quantize(x)
+    assert t.codes.is_contiguous() and t.scales.is_contiguous() and t.scales.data_ptr() % 16 == 0
+    assert t.codes.data_ptr() + t.codes.numel() <= t.scales.data_ptr()
+    kept, before = t.scales.clone(), (t.codes._version, t.scales._version)
+    codes = t.codes.clone()
+    t.codes.fill_(3)
+    assert torch.equal(t.scales, kept)
+    ecw.fp8_quantize(x, out=t)
+    assert torch.equal(t.codes, codes) and t.codes._version > before[0] + 1 and t.scales._version > before[1]
+    part = ecw.FP8Tensor(t.codes[2:5], t.scales[2:5], 3, 300)
+    assert torch.equal(part.dequantize(torch.float32), t.dequantize(torch.float32)[2:5])
+    with torch.inference_mode():
+        assert ecw.fp8_quantize(x).codes.is_inference() and ecw.rms_norm(x).is_inference()
+    keep = t.scales
+    del t, part  # the memory lives as long as one of them
+    torch.empty(7 * 384, dtype=torch.uint8, device="cuda").fill_(9)
+    assert torch.equal(keep, kept)
