@@ -256,6 +256,8 @@ extern "C" ecw_status rms_norm(ecw_stream stream, const ecw_rms_norm* n) {
     return refuse(ECW_E_INVALID_ARG, "residual and residual_out must be aligned device pointers");
   if (n->x_stride < 0 || (n->residual && (n->residual_stride < 0 || n->residual_out_stride < n->cols)))
     return refuse(ECW_E_INVALID_ARG, "row strides must not be negative, residual_out's at least cols");
+  if (n->residual && n->residual == n->residual_out && n->rows > 1 && n->residual_stride != n->residual_out_stride)
+    return refuse(ECW_E_INVALID_ARG, "in place the residual's strides must be the same");
   float shrink = 1.f;
   while (shrink * shrink * (float)n->cols > 1.f) shrink *= 0.5f;
   const NormArgs a{n->x, n->residual, n->weight, n->residual_out, n->y, static_cast<uint8_t*>(n->y_scales),

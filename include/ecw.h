@@ -467,8 +467,8 @@ ecw_status fp8_quantize(ecw_stream stream, const void* x, int dtype, int64_t x_s
  * even in fp16 (infinite past its range). */
 ecw_status fp8_dequantize(ecw_stream stream, const void* codes, const void* scales, uint32_t rows, uint32_t cols,
                           void* out, int out_dtype);
-/* y [batch][rows] (fp32, fp16 or bf16) = x w^T with both in the format; products exact, sums
- * in fp32, one rounding into y.  With a 16-bit y and more than a few rows of x up to 16
+/* y [batch][rows] (fp32, fp16 or bf16; 16-byte aligned) = x w^T with both in the format;
+ * products exact, sums in fp32, one rounding into y.  With a 16-bit y and more than a few rows of x up to 16
  * neighbouring products are added with 12 fraction bits under the largest one's power of two
  * before they go into the fp32 sum: 1.5e-5 to 7e-5 of the result (2-norm), a small part of
  * what rounding it to 16 bits takes.  The workspace need not be cleared; it is the call's
@@ -481,7 +481,8 @@ ecw_status fp8_gemm(ecw_stream stream, const void* w_codes, const void* w_scales
 /* y = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual, and h as the new
  * residual.  h is fp32 and rounded once, into residual_out; y is made of the unrounded h.
  * Strides in elements; y is dense, in a float type or in the 8-bit format (y its codes,
- * y_scales its scales).  residual_out may be residual itself, with the same stride. */
+ * y_scales its scales, both 16-byte aligned).  residual_out may be residual itself, with the
+ * same stride, y a dense x of its type; otherwise what is written lies apart from what is read. */
 typedef struct {
   const void* x;           /* [rows][cols], rows x_stride apart */
   const void* residual;    /* nullable, in x's type or fp32 */

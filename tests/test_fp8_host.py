@@ -93,7 +93,8 @@ def test_gemm_workspace(L):
     ({"x_dtype": 0}, INVALID), ({"y_dtype": ecw.DT_I8}, INVALID), ({"eps": -1.0}, INVALID), ({"eps": math.nan}, INVALID),
     ({"eps": math.inf}, INVALID), ({"residual": 0}, INVALID), ({"residual_out": 0}, INVALID), ({"residual": P + 2}, INVALID),
     ({"residual_out": P + 2}, INVALID), ({"residual_dtype": ecw.DT_F16}, UNSUPPORTED), ({"x_stride": -1}, INVALID),
-    ({"residual_stride": -1}, INVALID), ({"residual_out_stride": 63}, INVALID)])
+    ({"residual_stride": -1}, INVALID), ({"residual_out_stride": 63}, INVALID), ({"residual_stride": 128}, INVALID),
+    ({"residual_stride": 128, "rows": 0}, OK)])
 def test_norm(L, change, status):
     a = {"x": P, "residual": P, "weight": P, "residual_out": P, "y": P, "y_scales": P, "x_stride": 64, "residual_stride": 64,
          "residual_out_stride": 64, "rows": 2, "cols": 64, "x_dtype": ecw.DT_BF16, "residual_dtype": ecw.DT_F32,
