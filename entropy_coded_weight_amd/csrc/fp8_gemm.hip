@@ -487,7 +487,9 @@ Plan plan_tiles(uint32_t batch, uint32_t rows, uint32_t spans, bool exact, bool 
 }
 
 // Rows of w whose tiles fill the CUs for whole rounds, if the rest is better off in tiles of
-// another kind (4096 rows by 14336 x 4096: 896 tiles are three and a half rounds); else 0.
+// another kind (4096 rows by 14336 x 4096: 896 tiles are three and a half rounds, 222 us, cut
+// 214); else 0.  A second launch starts when the first has ended, which costs about 10 us
+// (1500 rows by 16384 x 2048 64.5 us cut, 60.5 not).
 uint32_t plan_cut(const Plan& p, uint32_t batch, uint32_t rows, uint32_t spans, bool exact) {
   const TileKind& t = exact ? kExact[p.kind] : kFast[p.kind];
   const uint64_t m = (batch + t.bm - 1) / t.bm, n = (rows + t.bn - 1) / t.bn, full = m * n / kCus;
@@ -496,7 +498,7 @@ uint32_t plan_cut(const Plan& p, uint32_t batch, uint32_t rows, uint32_t spans, 
   if (first == 0 || first >= n) return 0;
   const uint32_t cut = (uint32_t)(first * t.bn);
   const Plan rest = plan_tiles(batch, rows - cut, spans, exact, false);
-  return full * (1.f + spans * t.span) + 1.5f + rest.us < p.us ? cut : 0;
+  return full * (1.f + spans * t.span) + 1.5f + rest.us + 10.f < p.us ? cut : 0;
 }
 
 uint64_t part_size(uint32_t batch, uint32_t rows) { return ((uint64_t)batch * rows + 3) / 4 * 4; }

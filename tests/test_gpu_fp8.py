@@ -173,7 +173,8 @@ def test_product_of_whole_numbers_is_exact(batch, rows, cols):
 
 @pytest.mark.parametrize("batch,rows,cols", [(2048, 9000, 256), (4096, 4700, 130), (300, 14336, 512), (1500, 3001, 640), (17, 20000, 257),
                                              (16, 16, 30000), (4, 300, 20000), (40, 100, 25000), (33, 63, 20000), (19, 1, 9000),
-                                             (70, 2, 30000), (1, 3, 20001), (130, 130, 16385)])
+                                             (70, 2, 30000), (1, 3, 20001), (130, 130, 16385), (2048, 9000, 4096), (1043, 14511, 1800),
+                                             (538, 13235, 2300), (1000, 9000, 4000)])
 @pytest.mark.parametrize("out", DTYPES)
 def test_large_products_of_whole_numbers_are_exact(batch, rows, cols, out):
     """Tiles of every kind, rounds that are cut, columns in parts; the reference, fp32 sums of
