@@ -89,10 +89,10 @@ PyObject* py_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// gemm(codes, scales, cols, x codes, x scales, x cols, y or None, dtype) -> y
+// gemm(codes, scales, cols, x codes, x scales, x cols, y or None, dtype, short sums) -> y
 PyObject* py_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    expect(n, 8);
+    expect(n, 9);
     const at::Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
     const at::Tensor &xc = tensor(a[3], "x"), &xs = tensor(a[4], "x");
     const int64_t rows = codes.size(0), cols = whole(a[2], "cols", kMostCols), have = whole(a[5], "cols", kMostCols);
@@ -100,7 +100,11 @@ PyObject* py_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(xc, codes, "x", "tensor");
     const c10::DeviceGuard guard(codes.device());
     const at::ScalarType type = a[6] == Py_None ? dtype(a[7], "out_dtype") : tensor(a[6], "y").scalar_type();
-    const int yd = float_type(type, "y");
+    int yd = float_type(type, "y");
+    const int brief = PyObject_IsTrue(a[8]);
+    if (brief < 0) throw Raised{};
+    if (brief && yd == ECW_DT_F32) bad_value("short_sums are for float16 and bfloat16 results");
+    if (brief) yd |= ECW_FP8_SHORT_SUMS;
     const at::Tensor y = output(a[6], codes, {xc.size(0), rows}, type, "y");
     const uint32_t batch = size32(xc.size(0), "batch");
     size_t bytes = 0;

@@ -1,15 +1,16 @@
 // y[b][n] = sum_k x[b][k] w[n][k], both in the block-scaled 8-bit format.
 //
-// Two instructions multiply.  The scaled 8-bit one (16x16x128) takes one block of 128 columns
-// of 16 rows of each operand, 32 bytes a lane, and a scale byte of each lane's row, so that a
-// block's product takes one instruction, scales included (4.3 PFLOP/s measured, 2.1 for
-// bf16).  But it adds up to 16 neighbouring products with 12 fraction bits under the largest
-// one's power of two before they go into the fp32 sum: against 64 bits its sums are off by
-// 1.5e-5 of the result (2-norm, normal numbers), 7e-5 with columns a hundred times as large,
-// where fp32 sums are by 1e-7.  Next to an output rounded to 16 bits (1.7e-3 in bf16, 2e-4 in
-// fp16) that is nothing; an fp32 output shows it.  So fp32 outputs, and a few rows of x, which
-// are bound by reading w, go by the bf16 instruction (16x16x32): E4M3 numbers times their
-// scale are exact in bf16, products exact in fp32, and sums fp32.
+// Two instructions multiply.  The bf16 one (16x16x32) is what a call gets: E4M3 numbers times
+// their scale are exact in bf16, products exact in fp32, and sums fp32.  The scaled 8-bit one
+// (16x16x128) takes one block of 128 columns of 16 rows of each operand, 32 bytes a lane, and
+// a scale byte of each lane's row, so that a block's product takes one instruction, scales
+// included (4.3 PFLOP/s measured, 2.1 for bf16).  But it adds up to 16 neighbouring products
+// with 12 fraction bits under the largest one's power of two before they go into the fp32
+// sum: each may lose 2^-12 of the largest, so the sum up to 15 * 2^-12 < 2^-8 of the
+// products' magnitudes (448^2 - 448^2 + 2^2 is 0).  Measured against 64 bits 1.5e-5 of the
+// result in 2-norm for normal numbers, 7e-5 with columns a hundred times as large, where fp32
+// sums are off by 1e-7.  So it multiplies only where the caller asks for short sums, of
+// 16-bit outputs and more rows of x than go by k_fp8_gemm_few.
 //
 // Which of the columns of a block a lane holds is free as long as both operands agree and all
 // of a row's lanes give the same scale: lane l has row l % 16 and the 16-byte pieces l / 16
@@ -212,7 +213,7 @@ struct Fp8Tiles {
   static_assert((KG - 1) * kWaves * TM * TN * 1024 <= (int)kStage * NS, "");  // sums of the other groups
 };
 
-// EXACT: by the bf16 instruction.
+// EXACT: by the bf16 instruction, else by the 8-bit one.
 template <int WM, int WN, int TM, int TN, int NS, int KG, bool EXACT>
 __global__ void __launch_bounds__(64 * WM * WN * KG) k_fp8_gemm_tile(Fp8GemmArgs a, uint32_t m_tiles, uint32_t n_tiles,
                                                                      int y_dtype) {
@@ -487,8 +488,8 @@ Plan plan_tiles(uint32_t batch, uint32_t rows, uint32_t spans, bool exact, bool 
 }
 
 // Rows of w whose tiles fill the CUs for whole rounds, if the rest is better off in tiles of
-// another kind (4096 rows by 14336 x 4096: 896 tiles are three and a half rounds, 222 us, cut
-// 214); else 0.  A second launch starts when the first has ended, which costs about 10 us
+// another kind (4096 rows by 14336 x 4096 with short sums: 896 tiles are three and a half
+// rounds, 222 us, cut 214); else 0.  A second launch starts when the first has ended, which costs about 10 us
 // (1500 rows by 16384 x 2048 64.5 us cut, 60.5 not).
 uint32_t plan_cut(const Plan& p, uint32_t batch, uint32_t rows, uint32_t spans, bool exact) {
   const TileKind& t = exact ? kExact[p.kind] : kFast[p.kind];
@@ -506,7 +507,9 @@ uint64_t part_size(uint32_t batch, uint32_t rows) { return ((uint64_t)batch * ro
 ecw_status check_product(uint32_t rows, uint32_t cols, uint32_t batch, int y_dtype) {
   if (cols == 0 || cols > (1u << 30) || rows > (1u << 30)) return refuse(ECW_E_INVALID_ARG, "cols must be in [1, 2^30], rows at most 2^30");
   if (batch > (1u << 24)) return refuse(ECW_E_INVALID_ARG, "batch must be at most 2^24");
-  if (!is_float(y_dtype)) return refuse(ECW_E_INVALID_ARG, "y dtype must be F16, BF16 or F32");
+  const int dt = y_dtype & ~ECW_FP8_SHORT_SUMS;
+  if (!is_float(dt)) return refuse(ECW_E_INVALID_ARG, "y dtype must be F16, BF16 or F32");
+  if (dt != y_dtype && dt == ECW_DT_F32) return refuse(ECW_E_INVALID_ARG, "short sums are for F16 and BF16 outputs");
   return ECW_OK;
 }
 
@@ -522,7 +525,7 @@ ecw_status fp8_gemm_workspace_size(uint32_t rows, uint32_t cols, uint32_t batch,
   FewShape f;
   const uint32_t spans = fp8_row(cols) / 128;
   if (few_shape(batch, spans, &f)) return ECW_OK;
-  const Plan p = plan_tiles(batch, rows, spans, y_dtype == ECW_DT_F32);
+  const Plan p = plan_tiles(batch, rows, spans, !(y_dtype & ECW_FP8_SHORT_SUMS));
   if (p.splits > 1) *bytes = p.splits * part_size(batch, rows) * sizeof(float);
   return ECW_OK;
 }
@@ -539,9 +542,10 @@ ecw_status fp8_gemm(ecw_stream stream, const void* w_codes, const void* w_scales
                 static_cast<const uint8_t*>(x_codes), static_cast<const uint8_t*>(x_scales), y, rows, batch,
                 fp8_row(cols), fp8_scale_row(cols), fp8_row(cols) / 128, rows, 1, fp8_row(cols) / 128, nullptr, 0};
   const auto st = (hipStream_t)stream;
+  const bool exact = !(y_dtype & ECW_FP8_SHORT_SUMS);
+  y_dtype &= ~ECW_FP8_SHORT_SUMS;
   FewShape f;
   if (few_shape(batch, a.spans, &f)) return launch_few(st, a, f, y_dtype);
-  const bool exact = y_dtype == ECW_DT_F32;
   const Plan p = plan_tiles(batch, rows, a.spans, exact);
   if (p.splits > 1) {
     a.splits = p.splits, a.chunk = p.chunk, a.part_size = part_size(batch, rows);

@@ -64,8 +64,8 @@ __device__ __forceinline__ uint32_t spread(uint32_t t, uint32_t i) {
 }
 
 // The N neighbouring outputs of a lane, the first `left` of them.  Runs go out as wide wherever
-// they start (2444 rows of x by 10781 x 495 in 8 bits, fp16 outputs 38 us, with single elements
-// where rows are not aligned 104).
+// they start (2444 rows of x by 10781 x 495 in 8 bits with short sums, fp16 outputs 38 us, with
+// single elements where rows are not aligned 104).
 template <int DT, int N>
 __device__ __forceinline__ void store_run(void* y, uint64_t at, const float (&v)[N], uint32_t left) {
   if (left < N) {

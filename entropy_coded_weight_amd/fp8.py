@@ -59,19 +59,22 @@ class FP8Tensor:
             return on(stream, (self.codes, self.scales, out), lambda: self.dequantize(dtype, out))
         return native("_fp8").dequantize(self.codes, self.scales, self.cols, dtype, out)
 
-    def gemm(self, x: FP8Tensor, y=None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    def gemm(self, x: FP8Tensor, y=None, out_dtype=torch.float32, stream=None, short_sums: bool = False) -> torch.Tensor:
         """y = x W^T for any batch: x an FP8Tensor [batch, cols]; y [batch, rows], fp32 unless
-        out_dtype (fp16, bf16) says otherwise.
+        out_dtype (fp16, bf16) says otherwise; one that is given starts at a multiple of 16 bytes.
 
-        An fp32 result has fp32 sums of exact products.  For a 16-bit one of more than a few
-        rows up to 16 neighbouring products are added with 12 fraction bits under the largest
-        one's power of two first: 1.5e-5 to 7e-5 of the result in 2-norm, a small part of its
-        own rounding; where large products cancel, ask for fp32."""
+        Products are exact, sums fp32, in an order that depends on the shape, and rounded once.
+        short_sums, for 16-bit results: up to 16 neighbouring products may be added with 12
+        fraction bits under the largest one's power of two first, in about half the time for
+        many rows.  A sum is then off by up to 2^-8 of its products' magnitudes (1.5e-5 to 7e-5
+        of the result in 2-norm measured on normal numbers and with large columns): not where
+        large products cancel."""
         if not isinstance(x, FP8Tensor):
             raise TypeError("x must be an FP8Tensor: fp8_quantize(x), or a norm's 8-bit output")
         if stream is not None:
-            return on(stream, (self.codes, self.scales, y, x.codes, x.scales), lambda: self.gemm(x, y, out_dtype))
-        return native("_fp8").gemm(self.codes, self.scales, self.cols, x.codes, x.scales, x.cols, y, out_dtype)
+            return on(stream, (self.codes, self.scales, y, x.codes, x.scales),
+                      lambda: self.gemm(x, y, out_dtype, short_sums=short_sums))
+        return native("_fp8").gemm(self.codes, self.scales, self.cols, x.codes, x.scales, x.cols, y, out_dtype, short_sums)
 
 
 def _tensor(codes, scales, cols):

@@ -467,12 +467,16 @@ ecw_status fp8_quantize(ecw_stream stream, const void* x, int dtype, int64_t x_s
  * even in fp16 (infinite past its range). */
 ecw_status fp8_dequantize(ecw_stream stream, const void* codes, const void* scales, uint32_t rows, uint32_t cols,
                           void* out, int out_dtype);
+/* With a 16-bit y_dtype of fp8_gemm: sums may be shorter than fp32. */
+#define ECW_FP8_SHORT_SUMS 0x100
 /* y [batch][rows] (fp32, fp16 or bf16; 16-byte aligned) = x w^T with both in the format;
- * products exact, sums in fp32, one rounding into y.  With a 16-bit y and more than a few rows of x up to 16
- * neighbouring products are added with 12 fraction bits under the largest one's power of two
- * before they go into the fp32 sum: 1.5e-5 to 7e-5 of the result (2-norm), a small part of
- * what rounding it to 16 bits takes.  The workspace need not be cleared; it is the call's
- * until its work is done. */
+ * products exact, sums in fp32 (in an order that depends on the shape), one rounding into y.
+ * With y_dtype ECW_DT_F16 or ECW_DT_BF16 | ECW_FP8_SHORT_SUMS up to 16 neighbouring products
+ * may be added with 12 fraction bits under the largest one's power of two before they go into
+ * the fp32 sum, which takes about half the time for many rows of x.  Such a sum is off by up to
+ * 2^-8 of the sum of the products' magnitudes: not for products that cancel.  (Measured: 1.5e-5
+ * of the result in 2-norm for normal numbers, 7e-5 with columns a hundred times as large.)
+ * The workspace need not be cleared; it is the call's until its work is done. */
 ecw_status fp8_gemm_workspace_size(uint32_t rows, uint32_t cols, uint32_t batch, int y_dtype, size_t* bytes);
 ecw_status fp8_gemm(ecw_stream stream, const void* w_codes, const void* w_scales, uint32_t rows, uint32_t cols,
                     const void* x_codes, const void* x_scales, uint32_t batch, void* y, int y_dtype, void* workspace,

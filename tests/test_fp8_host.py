@@ -152,3 +152,14 @@ def test_calls_refuse_tensors_off_the_gpu():
                  lambda: ecw.rms_norm([1.0]), lambda: ecw.FP8Tensor(x, x, 2, 64), lambda: ecw.Rotary(64, device="cpu")):
         with pytest.raises(TypeError):
             call()
+
+
+def test_short_sums_are_for_16_bit_outputs(L):
+    short, n = 0x100, ctypes.c_size_t(7)
+    args = (None, P, P, 16, 64, P, P, 0, P)
+    for dt, status in ((ecw.DT_F16, OK), (ecw.DT_BF16, OK), (ecw.DT_F32, INVALID), (ecw.DT_I8, INVALID), (0, INVALID)):
+        assert L.fp8_gemm(*args, dt | short, P, 1 << 40) == status
+        assert L.fp8_gemm_workspace_size(16, 64, 0, dt | short, n) == status and n.value == 0
+    assert L.fp8_gemm(*args, ecw.DT_F16 | 0x200, P, 1 << 40) == INVALID
+    for dt in (ecw.DT_F16, ecw.DT_F16 | short):  # few tiles, many columns: parts either way
+        assert L.fp8_gemm_workspace_size(64, 16384, 40, dt, n) == OK and n.value > 0
