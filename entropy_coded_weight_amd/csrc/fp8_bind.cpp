@@ -1,7 +1,6 @@
 // Python binding of the 8-bit matrices, the root-mean-square norm and the rotary positions.
-#include <ATen/MemoryOverlap.h>
-
 #include "bind_common.h"
+#include "overlap.h"
 
 namespace {
 
@@ -16,14 +15,15 @@ struct Api {
 
 constexpr int64_t kMostCols = 1 << 30;
 
-// What a call writes next to what it reads must be the same elements or none of them.
+ecw::Box box(const at::Tensor& t) {
+  return ecw::box_of(t.data_ptr(), t.element_size(), t.sizes().data(), t.strides().data(), t.dim());
+}
+// What a call writes next to what it reads must be none of its bytes, or (`same`) the same elements.
 void apart(const at::Tensor& out, const at::Tensor& in, const char* out_name, const char* in_name, bool same = false) {
-  const at::MemOverlapStatus s = at::get_overlap_status(out, in);
-  const bool one = out.data_ptr() == in.data_ptr() && out.numel() && in.numel();
-  const bool alike = one && out.scalar_type() == in.scalar_type() && out.sizes() == in.sizes() && out.strides() == in.strides();
-  if (alike && same) return;
-  if (one || s == at::MemOverlapStatus::Full || s == at::MemOverlapStatus::Partial)
-    bad_value(std::string(out_name) + " overlaps " + in_name);
+  if (same && out.data_ptr() == in.data_ptr() && out.scalar_type() == in.scalar_type() && out.sizes() == in.sizes() &&
+      out.strides() == in.strides())
+    return;
+  if (ecw::boxes_meet(box(out), box(in))) bad_value(std::string(out_name) + " overlaps " + in_name);
 }
 
 struct Eight {
@@ -43,7 +43,9 @@ Eight eight_bits(PyObject* codes, PyObject* scales, const at::Tensor& like, int6
     const at::Tensor all = fresh({rows * (wide + scale_wide)}, at::kByte, like);
     return {bytes_of(all, 0, rows, wide), bytes_of(all, rows * wide, rows, scale_wide)};
   }
-  return {output(codes, like, {rows, wide}, at::kByte, "codes"), output(scales, like, {rows, scale_wide}, at::kByte, "scales")};
+  const Eight out{output(codes, like, {rows, wide}, at::kByte, "codes"), output(scales, like, {rows, scale_wide}, at::kByte, "scales")};
+  apart(out.codes, out.scales, "codes", "scales");
+  return out;
 }
 
 // quantize(x, gate or None, codes or None, scales or None) -> codes, scales, cols
@@ -54,19 +56,22 @@ PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int xd = float_type(x.scalar_type(), "x");
     const Matrix m = matrix(x, "x", "[rows, cols] with at least one column");
     if (m.cols == 0) bad_value("x must be [rows, cols] with at least one column");
-    const void* gate = nullptr;
+    const at::Tensor* gate = nullptr;
     int64_t gate_stride = 0;
     if (a[1] != Py_None) {
-      const at::Tensor& g = tensor(a[1], "gate");
-      same_device(g, x, "gate", "tensor");
-      if (g.sizes() != x.sizes() || g.scalar_type() != x.scalar_type()) bad_value("gate must have x's shape and dtype");
-      gate_stride = matrix(g, "gate", "[rows, cols]").stride;
-      gate = g.data_ptr();
+      gate = &tensor(a[1], "gate");
+      same_device(*gate, x, "gate", "tensor");
+      if (gate->sizes() != x.sizes() || gate->scalar_type() != x.scalar_type()) bad_value("gate must have x's shape and dtype");
+      gate_stride = matrix(*gate, "gate", "[rows, cols]").stride;
     }
     const c10::DeviceGuard guard(x.device());
     const Eight out = eight_bits(a[2], a[3], x, m.rows, m.cols);
-    check(api.quantize(stream_of(x.device()), x.data_ptr(), xd, m.stride, gate, gate_stride, size32(m.rows, "rows"),
-                       size32(m.cols, "cols"), out.codes.data_ptr(), out.scales.data_ptr()),
+    if (a[2] != Py_None) {
+      apart(out.codes, x, "codes", "x"), apart(out.scales, x, "scales", "x");
+      if (gate) apart(out.codes, *gate, "codes", "gate"), apart(out.scales, *gate, "scales", "gate");
+    }
+    check(api.quantize(stream_of(x.device()), x.data_ptr(), xd, m.stride, gate ? gate->data_ptr() : nullptr, gate_stride,
+                       size32(m.rows, "rows"), size32(m.cols, "cols"), out.codes.data_ptr(), out.scales.data_ptr()),
           "fp8_quantize");
     return Py_BuildValue("NNL", THPVariable_Wrap(out.codes), THPVariable_Wrap(out.scales), (long long)m.cols);
   });
@@ -82,6 +87,7 @@ PyObject* py_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = a[4] == Py_None ? dtype(a[3], "dtype") : tensor(a[4], "out").scalar_type();
     const int od = float_type(type, "out");
     const at::Tensor out = output(a[4], codes, {rows, cols}, type, "out");
+    if (a[4] != Py_None) apart(out, codes, "out", "codes"), apart(out, scales, "out", "scales");
     check(api.dequantize(stream_of(codes.device()), codes.data_ptr(), scales.data_ptr(), (uint32_t)rows,
                          (uint32_t)cols, out.data_ptr(), od),
           "fp8_dequantize");
@@ -106,6 +112,8 @@ PyObject* py_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (brief && yd == ECW_DT_F32) bad_value("short_sums are for float16 and bfloat16 results");
     if (brief) yd |= ECW_FP8_SHORT_SUMS;
     const at::Tensor y = output(a[6], codes, {xc.size(0), rows}, type, "y");
+    if (a[6] != Py_None)
+      for (const at::Tensor* in : {&codes, &scales, &xc, &xs}) apart(y, *in, "y", in == &xc || in == &xs ? "x" : "the tensor");
     const uint32_t batch = size32(xc.size(0), "batch");
     size_t bytes = 0;
     check(api.workspace((uint32_t)rows, (uint32_t)cols, batch, yd, &bytes), "fp8_gemm_workspace_size");
@@ -256,7 +264,7 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t.sizes() != in.sizes() || t.scalar_type() != in.scalar_type())
         bad_value(std::string(name) + " must have " + in_name + "'s shape and dtype");
       if (t.stride(2) != 1 && dim > 1) bad_type(std::string(name) + " must have a unit inner stride");
-      if (at::has_internal_overlap(t) == at::MemOverlap::Yes) bad_value(std::string(name) + " overlaps itself");
+      if (box(t).folded) bad_value(std::string(name) + " overlaps itself");
       apart(t, in, name, in_name, true);
       apart(t, at, name, "positions");
       written(t);

@@ -14,6 +14,7 @@ records a gradient, and an input that requires one is used as its values.
 
 Work runs on the current stream of the operands' device, or on `stream`, one of the same
 device; results are allocated there.  Whoever passes a stream orders it after the producers of the operands.
+A given output that overlaps an operand is refused, but where a call says that it works in place.
 """
 from __future__ import annotations
 
