@@ -100,10 +100,14 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs
     X x[OCTS];
     R r[DR ? OCTS : 1];
   };
-  // rows past the last are computed as the last, so that every lane takes as many turns
-  auto row_of = [&](uint32_t first) { return min(first + threadIdx.x / LANES, a.rows - 1); };
+  auto row_of = [&](uint32_t first) { return kRows == 1 ? first : first + threadIdx.x / LANES; };
+  // Only rows that there are are asked for: a residual that is written in place has another
+  // lane's stores in it.  Lanes behind the last row take their turns over whatever they hold.
+  // (Blocks of one row with registers for the next need no look here: each has a first row, and
+  // the loop below looks before it asks.)
   auto ask = [&](Row& to, uint32_t first) {
     const uint32_t row = row_of(first);
+    if ((kRows > 1 || !kHold) && row >= a.rows) return;
 #pragma unroll
     for (int j = 0; j < OCTS; ++j) {
       const uint32_t c = (lane + j * LANES) * 8;
@@ -113,6 +117,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs
     }
   };
   Row raw;
+  if constexpr (kRows > 1 || !kHold) raw = {};
   ask(raw, blockIdx.x * kRows);
   float w[kHold ? OCTS : 1][8];
   if constexpr (kHold) {
@@ -131,8 +136,8 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs
   }
   uint32_t turn = 0;
   for (uint32_t first = blockIdx.x * kRows; first < a.rows; first += gridDim.x * kRows, turn ^= 1) {
-    const bool real = first + threadIdx.x / LANES < a.rows;
     const uint32_t row = row_of(first);
+    const bool real = kRows == 1 || row < a.rows;
     float h[OCTS][8];
     float sum = 0.f;
 #pragma unroll
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs
         sum = fmaf(u, u, sum);
       }
     }
-    if constexpr (kHold) ask(raw, first + gridDim.x * kRows);
+    if (kHold && first + gridDim.x * kRows < a.rows) ask(raw, first + gridDim.x * kRows);
     const float m = row_sum<LANES>(sum, sums, turn) * a.mean + a.eps;
     const bool tiny = m < 0x1p-96f;  // the instruction takes no subnormal numbers
     const float f = __builtin_amdgcn_rsqf(tiny ? m * 0x1p96f : m) * (tiny ? 0x1p48f : 1.f);
@@ -190,8 +195,7 @@ __global__ void __launch_bounds__(LANES < 256 ? 256 : LANES) k_rms_norm(NormArgs
           store_values<ECW_DT_F32>(a.y, at, v, n);
       }
     }
-    if constexpr (!kHold)
-      if (first + gridDim.x * kRows < a.rows) ask(raw, first + gridDim.x * kRows);
+    if (!kHold) ask(raw, first + gridDim.x * kRows);
   }
 }
 

@@ -68,6 +68,23 @@ def test_norm_takes_outputs_between_its_inputs():
     assert torch.equal(y, want) and torch.equal(buf[1:8:2, :512], h) and torch.equal(buf[::2], kept[::2])
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 64), (5, 64), (33001, 128), (33001, 40), (9003, 500), (5001, 1000), (2500, 2048), (2101, 4096),
+                                       (2050, 8192), (600, 30000)])
+def test_norm_in_place_of_many_rows(rows, cols):
+    """Each row is read by the lanes that write it and no others: the residual over itself, and the
+    result over x, are what they are apart."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, generator=g, device="cuda").bfloat16()
+    for dtype in (torch.bfloat16, torch.float32):
+        r = torch.randn(rows, cols, generator=g, device="cuda").to(dtype)
+        for out in (EIGHT, torch.bfloat16):
+            want, h = ecw.rms_norm(x, residual=r, out_dtype=out)
+            over, z = r.clone(), x.clone()
+            y, got = ecw.rms_norm(z, residual=over, residual_out=over, **({"out_dtype": out} if out is EIGHT else {"out": z}))
+            assert got.data_ptr() == over.data_ptr() and torch.equal(over, h)
+            assert torch.equal(y.codes, want.codes) and torch.equal(y.scales, want.scales) if out is EIGHT else torch.equal(z, want)
+
+
 def test_rotary_refuses_outputs_across_its_inputs():
     qkv = _randn(9, 8, 64, seed=1)
     kept, at, r = qkv.clone(), torch.arange(9, dtype=torch.int32, device="cuda"), ecw.Rotary(64)
