@@ -460,7 +460,7 @@ ecw_status kv4_attend(ecw_stream stream, const ecw_kv4* cache, const ecw_kv4_row
 
 /* x [rows][cols] fp16, bf16 or fp32, x_stride elements apart -> codes, scales.  With a gate
  * (same type and shape; else NULL) it is silu(gate) * x that is quantised, computed in fp32:
- * silu(g) = g / (1 + e^-g), zero below g = -88. */
+ * silu(g) = g / (1 + e^-g), zero below g = -88.73, where e^-g passes fp32's range. */
 ecw_status fp8_quantize(ecw_stream stream, const void* x, int dtype, int64_t x_stride, const void* gate,
                         int64_t gate_stride, uint32_t rows, uint32_t cols, void* codes, void* scales);
 /* The values as a dense [rows][cols] matrix: exact in fp32 and bf16, rounded to nearest

@@ -388,3 +388,28 @@ def test_codes_and_scales_are_tensors_of_their_own():
     del t, part  # the memory lives as long as one of them
     torch.empty(7 * 384, dtype=torch.uint8, device="cuda").fill_(9)
     assert torch.equal(keep, kept)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gate_up_to_where_the_exponential_passes_fp32(dtype):
+    """e^-g is a number up to g = -88.72, so the gate is one too, though 1 + e^-g has a reciprocal
+    under 2^-126 from -87.34 on; behind -88.73 it is zero.  Blocks of such gates alone."""
+    shut = torch.tensor([-87.0, -87.3, -87.33, -87.34, -87.4, -87.5, -87.9, -88.0, -88.1, -88.3, -88.5, -88.6, -88.7]).to(dtype)
+    shut = shut[shut > -88.722]  # -88.7 in bf16 is -88.5
+    g = shut[torch.arange(3 * 128) % len(shut)].view(3, 128)
+    x = ((_randn(3, 128, seed=1).abs() + 0.5) * torch.tensor([[1.0], [-100.0], [1e4 if dtype == torch.float16 else 1e30]])).to(dtype)
+    t = ecw.fp8_quantize(x.cuda(), gate=g.cuda())
+    want = _f64(x) * _f64(g) / (1 + np.exp(-_f64(g)))
+    assert R.between(_f64(t.dequantize(torch.float32)), want, 2.0 ** -21).all()
+    g = torch.tensor([-88.75, -89.0, -100.0, -1000.0, -60000.0]).to(dtype)
+    t = ecw.fp8_quantize(torch.full((1, 5), 100.0, dtype=dtype, device="cuda"), gate=g[None].cuda())
+    assert (t.dequantize(torch.float32) == 0).all()
+
+
+def test_gate_of_the_largest_and_smallest_numbers():
+    """Neither a large nor a small gate leaves fp32's range on the way."""
+    g = torch.tensor([[3.4e38, 1e38, 2.0 ** 126, 2.0 ** 125, 1e30] * 26, [2.0 ** -126, -2.0 ** -126, 2.0 ** -120, 1e-30, -1e-30] * 26])[:, :128].contiguous()
+    x = torch.tensor([[1.0], [1e35]]).expand(2, 128).contiguous()
+    t = ecw.fp8_quantize(x.cuda(), gate=g.cuda())
+    want = _f64(x) * _f64(g) / (1 + np.exp(-np.minimum(_f64(g), 700)))
+    assert R.between(_f64(t.dequantize(torch.float32)), want, 2.0 ** -21).all()
