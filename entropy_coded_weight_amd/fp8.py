@@ -180,9 +180,9 @@ class Rotary:
         """q [rows, heads, head_dim] and k (or None), fp16/bf16/fp32 at any strides of rows and
         heads, turned by positions, int32 or int64 [rows] or [axes, rows].  Gives (q, k), or q
         alone; out=(q, k) writes in place."""
-        if stream is not None:
-            return on(stream, (q, k, positions, self.freqs, self.axis_of, *(out or ())), lambda: self(q, k, positions, out))
         q_out, k_out = (None, None) if out is None else (out, None) if isinstance(out, torch.Tensor) else out
+        if stream is not None:
+            return on(stream, (q, k, positions, self.freqs, self.axis_of, q_out, k_out), lambda: self(q, k, positions, (q_out, k_out)))
         return native("_fp8").rotary(q, k, positions, self.freqs, self.axis_of, self.axes, self.head_dim, self.neighbours,
                                      self.scale, q_out, k_out)
 

@@ -144,3 +144,15 @@ def test_matrices_refuse_outputs_over_their_inputs():
     assert ecw.fp8_quantize(x, gate=g, out=t) is t and torch.equal(t.codes, want.codes) and torch.equal(t.scales, want.scales)
     got = t.gemm(t, y[:64].view(8, 8))
     assert got.data_ptr() == y.data_ptr() and torch.equal(got, want.gemm(want)) and (y[64:] == 0).all()
+
+
+def test_rotary_into_one_tensor_on_another_stream():
+    q, at, r = _randn(5, 3, 64, seed=1), torch.arange(5, dtype=torch.int32, device="cuda"), ecw.Rotary(64)
+    want, side = r(q, None, at), torch.cuda.Stream()
+    y, one = torch.zeros_like(q), torch.zeros_like(q[:, :1])
+    side.wait_stream(torch.cuda.current_stream())
+    got = r(q, None, at, out=y, stream=side)
+    both = r(q, q[:, :1], at, out=(None, one), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert got.data_ptr() == y.data_ptr() and torch.equal(y, want)
+    assert torch.equal(both[0], want) and torch.equal(one, want[:, :1])
