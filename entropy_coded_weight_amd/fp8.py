@@ -95,11 +95,12 @@ def fp8_quantize(x: torch.Tensor, gate: torch.Tensor | None = None, out: FP8Tens
                  stream=None) -> FP8Tensor:
     """x fp16/bf16/fp32 [rows, cols] (or [cols]), rows at any stride, as an FP8Tensor; with a
     gate of x's shape and dtype, silu(gate) * x."""
+    if out is not None:
+        _fits(out, x)
     if stream is not None:
         used = (x, gate) if out is None else (x, gate, out.codes, out.scales)
         return on(stream, used, lambda: fp8_quantize(x, gate, out))
     if out is not None:
-        _fits(out, x)
         native("_fp8").quantize(x, gate, out.codes, out.scales)
         return out
     return _tensor(*native("_fp8").quantize(x, gate, None, None))

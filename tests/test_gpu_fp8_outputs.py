@@ -156,3 +156,18 @@ def test_rotary_into_one_tensor_on_another_stream():
     torch.cuda.current_stream().wait_stream(side)
     assert got.data_ptr() == y.data_ptr() and torch.equal(y, want)
     assert torch.equal(both[0], want) and torch.equal(one, want[:, :1])
+
+
+def test_refusals_are_the_same_on_a_stream():
+    x, side = torch.ones(4, 256, device="cuda"), torch.cuda.Stream()
+    t = ecw.fp8_quantize(x)
+    for stream in (None, side):
+        for call, error in [(lambda: ecw.fp8_quantize(x, out=x, stream=stream), TypeError),
+                            (lambda: ecw.fp8_quantize(x, out=[t], stream=stream), TypeError),
+                            (lambda: ecw.fp8_quantize([1.0], out=t, stream=stream), ValueError),
+                            (lambda: ecw.fp8_quantize(x[:2], out=t, stream=stream), ValueError),
+                            (lambda: ecw.rms_norm(x, out=x, out_dtype=EIGHT, stream=stream), TypeError),
+                            (lambda: t.gemm(x, stream=stream), TypeError), (lambda: t.gemm(t, y=x, stream=stream), ValueError),
+                            (lambda: t.gemm(t, stream=stream, short_sums=True), ValueError)]:
+            with pytest.raises(error):
+                call()
