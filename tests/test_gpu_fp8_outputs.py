@@ -24,6 +24,9 @@ def _randn(*shape, seed=0, dtype=torch.float32):
     return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
 
 
+DTYPES = [torch.float16, torch.bfloat16, torch.float32]
+
+
 def _eight(store, at, rows, cols):
     """An FP8Tensor in `store`'s bytes from `at` on: codes, then scales."""
     codes, scales = rows * (-(-cols // 128) * 128), rows * (-(-cols // 2048) * 16)
@@ -171,3 +174,62 @@ def test_refusals_are_the_same_on_a_stream():
                             (lambda: t.gemm(t, stream=stream, short_sums=True), ValueError)]:
             with pytest.raises(error):
                 call()
+
+
+def _between_guards(shape, dtype, offset=64):
+    """A tensor that starts 16-byte aligned and ends right before what must stay 7: (it, all)."""
+    n = shape[0] * shape[1]
+    store = torch.full((offset + n + 4096,), 7, dtype=dtype, device="cuda")
+    y = store[offset:offset + n].view(shape)
+    assert y.data_ptr() % 16 == 0
+    return y, store
+
+
+def _untouched(y, store):
+    first = y.storage_offset()
+    return (store[:first] == 7).all() and (store[first + y.numel():] == 7).all()
+
+
+@pytest.mark.parametrize("out,short", [(t, False) for t in DTYPES] + [(t, True) for t in DTYPES[:2]])
+@pytest.mark.parametrize("batch,rows,cols", [
+    (1, 1, 300), (3, 50, 200), (5, 13, 2000), (16, 31, 500), (16, 33, 8192), (17, 70, 200), (20, 70, 200), (40, 63, 20000), (33, 1, 9000),
+    (41, 3, 30000), (65, 127, 16384), (70, 130, 200), (129, 257, 300), (300, 260, 200), (301, 259, 4000), (1000, 2049, 130),
+    (2049, 4999, 130), (4097, 3585, 128)])
+def test_product_writes_its_output_only(batch, rows, cols, out, short):
+    """The kernel for few rows, tiles of both instructions, parts of the columns and their join, and
+    rounds that are cut: with ragged ends, every element and none before or behind."""
+    g = torch.Generator().manual_seed(batch)
+    x, w = (torch.randint(-1, 2, (n, cols), generator=g).float().cuda() for n in (batch, rows))
+    y, store = _between_guards((batch, rows), out)
+    got = ecw.fp8_quantize(w).gemm(ecw.fp8_quantize(x), y=y, short_sums=short)
+    assert got.data_ptr() == y.data_ptr() and torch.equal(y, (x @ w.t()).to(out))  # whole numbers under 2^24
+    assert _untouched(y, store)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 127), (5, 129), (2, 1001), (33, 333), (3, 16390)])
+def test_quantise_dequantise_and_norm_write_their_outputs_only(rows, cols, dtype):
+    x = _randn(rows, cols, seed=1, dtype=dtype)
+    want = ecw.fp8_quantize(x)
+    codes, all_codes = _between_guards(tuple(want.codes.shape), torch.uint8)
+    scales, all_scales = _between_guards(tuple(want.scales.shape), torch.uint8)
+    t = ecw.fp8_quantize(x, out=ecw.FP8Tensor(codes, scales, rows, cols))
+    assert torch.equal(codes, want.codes) and torch.equal(scales, want.scales)
+    assert _untouched(codes, all_codes) and _untouched(scales, all_scales)
+    for out in DTYPES:
+        for offset in (64, 67):
+            store = torch.full((offset + rows * cols + 100,), 7, dtype=out, device="cuda")
+            y = store[offset:offset + rows * cols].view(rows, cols)
+            t.dequantize(out=y)
+            assert torch.equal(y, want.dequantize(out)) and _untouched(y, store)
+            y.fill_(7)
+            ecw.rms_norm(x, out=y)
+            assert torch.equal(y, ecw.rms_norm(x, out_dtype=out)) and _untouched(y, store)
+    want = ecw.rms_norm(x, residual=x, out_dtype=EIGHT)[0]
+    wide = torch.full((rows + 2, cols + 9), 7, dtype=dtype, device="cuda")
+    ecw.rms_norm(x, residual=x, residual_out=wide[1:-1, 4:-5], out=t)
+    assert torch.equal(codes, want.codes) and torch.equal(scales, want.scales)
+    assert _untouched(codes, all_codes) and _untouched(scales, all_scales)
+    assert torch.equal(wide[1:-1, 4:-5], (x.float() + x.float()).to(dtype))
+    wide[1:-1, 4:-5] = 7
+    assert (wide == 7).all()

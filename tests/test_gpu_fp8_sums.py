@@ -98,3 +98,93 @@ def test_short_sums_are_refused_for_fp32():
         with pytest.raises(ValueError):
             t.gemm(t, y, short_sums=True)
     assert (t.gemm(t, torch.zeros(4, 4, dtype=torch.float16, device="cuda"), short_sums=True) == 256).all()
+
+
+# Both instructions, and 16-bit outputs of both.
+SUMS = [(torch.bfloat16, False), (torch.bfloat16, True), (torch.float16, False), (torch.float16, True)]
+BATCHES = [1, 16, 17, 20, 70, 300]
+
+
+@pytest.mark.parametrize("out,short", SUMS)
+@pytest.mark.parametrize("batch", BATCHES)
+def test_nan_blocks(batch, out, short):
+    """A NaN block of w is NaN in its row's outputs, one of x in its own row; no others."""
+    x, w = _whole(batch, 300, 3, 1), _whole(40, 300, 3, 2)
+    x[batch - 1, 290], w[7, 5], w[39, 130] = float("inf"), float("nan"), float("-inf")
+    y = ecw.fp8_quantize(w.cuda()).gemm(ecw.fp8_quantize(x.cuda()), out_dtype=out, short_sums=short).cpu()
+    bad = torch.zeros(batch, 40, dtype=torch.bool)
+    bad[batch - 1] = True
+    bad[:, [7, 39]] = True
+    assert torch.equal(torch.isnan(y), bad)
+    x[batch - 1, 256:], w[7, :128], w[39, 128:256] = 0, 0, 0
+    assert torch.equal(y[~bad], (x.double() @ w.double().t()).to(out)[~bad])
+
+
+@pytest.mark.parametrize("out,short", SUMS)
+@pytest.mark.parametrize("batch", BATCHES)
+def test_nan_scales_over_numbers(batch, out, short):
+    """The scale byte alone makes a block NaN, whatever its codes, zeros among them."""
+    xv = _whole(batch, 300, 3, 1)
+    xv[0, 256:] = 0
+    x, w = ecw.fp8_quantize(xv.cuda()), ecw.fp8_quantize(_whole(40, 300, 3, 2).cuda())
+    x.scales[0, 2] = 255
+    w.scales[11, 0] = 255
+    bad = torch.zeros(batch, 40, dtype=torch.bool)
+    bad[0], bad[:, 11] = True, True
+    assert torch.equal(torch.isnan(w.gemm(x, out_dtype=out, short_sums=short)).cpu(), bad)
+
+
+@pytest.mark.parametrize("out,short", SUMS)
+@pytest.mark.parametrize("batch", BATCHES)
+def test_nan_codes(batch, out, short):
+    """A code that is NaN beside numbers, with a scale of its block's: of either sign."""
+    x, w = ecw.fp8_quantize(_whole(batch, 300, 3, 1).cuda()), ecw.fp8_quantize(_whole(40, 300, 3, 2).cuda())
+    x.codes[batch - 1, 130], w.codes[3, 17], w.codes[38, 299] = 0x7f, 0xff, 0x7f
+    bad = torch.zeros(batch, 40, dtype=torch.bool)
+    bad[batch - 1], bad[:, [3, 38]] = True, True
+    assert torch.equal(torch.isnan(w.gemm(x, out_dtype=out, short_sums=short)).cpu(), bad)
+
+
+@pytest.mark.parametrize("short", [False, True])
+@pytest.mark.parametrize("batch", BATCHES)
+def test_ends_of_the_range(batch, short):
+    """Scales at both ends of their range: sums that pass fp32 are infinite, of their own sign,
+    products under it vanish, and what lies between is exact."""
+    def product(a, b):
+        return ecw.fp8_quantize(torch.full((32, 256), b, device="cuda")).gemm(
+            ecw.fp8_quantize(torch.full((batch, 256), a, device="cuda")), out_dtype=torch.bfloat16, short_sums=short).cpu()
+    v = R.rounded(np.full((1, 256), np.float64(np.float32(3e38))))[0, 0]
+    assert torch.equal(product(3e38, 2.0 ** -100), torch.full((batch, 32), v * 2.0 ** -100 * 256, dtype=torch.float64).bfloat16())
+    assert torch.equal(product(2.0 ** -117, 2.0 ** 100), torch.full((batch, 32), 2.0 ** -9, dtype=torch.bfloat16))
+    assert (product(3e38, 3e38) == float("inf")).all() and (product(-3e38, 3e38) == float("-inf")).all()
+    assert (product(2.0 ** -100, 2.0 ** -100) == 0).all()
+
+
+@pytest.mark.parametrize("out,short", SUMS)
+@pytest.mark.parametrize("batch", [3, 40, 300])
+def test_two_streams_and_two_graphs_at_once(batch, out, short):
+    """Calls that overlap share nothing: the same weights on two streams, and two graphs of them
+    replayed in turn."""
+    w = ecw.fp8_quantize(_whole(100, 20000, 1, 1).cuda())
+    xs = [ecw.fp8_quantize(_whole(batch, 20000, 1, 2 + i).cuda()) for i in range(2)]
+    want = [w.gemm(x).to(out) for x in xs]  # whole numbers, exact in every order
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[w.gemm(xs[i], out_dtype=out, short_sums=short, stream=streams[i]) for i in range(2)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for turn in got for i, y in enumerate(turn))
+    graphs, held = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            held.append(w.gemm(xs[i], out_dtype=out, short_sums=short))
+    for _ in range(3):
+        for y in held:
+            y.zero_()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                streams[i].wait_stream(torch.cuda.default_stream())
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(held[i], want[i]) for i in range(2))
