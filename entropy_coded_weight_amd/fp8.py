@@ -141,8 +141,9 @@ class Rotary:
     (rotary_dim / 2 numbers, used as their float64 values): base ** (-2 j / rotary_dim).
     With several axes each pair follows the position on one: `sections` says how many pairs
     each axis has, one after the other, `axes` the axis of every pair.  scale multiplies
-    the result.  Angles are exact to 2^-32 of a turn at any position, of either sign, so
-    negated positions undo a turn (and give the gradient of one)."""
+    what is turned.  Angles are within 2^-32 of a turn for positions up to 2^32 of either sign,
+    and within 2^-64 of it times the position beyond, so negated positions undo a turn (and give
+    the gradient of one)."""
 
     def __init__(self, head_dim: int, rotary_dim: int | None = None, base: float = 10000.0, inv_freq=None,
                  sections=None, axes=None, neighbours: bool = False, scale: float = 1.0, device="cuda"):

@@ -484,6 +484,8 @@ ecw_status fp8_gemm(ecw_stream stream, const void* w_codes, const void* w_scales
 
 /* y = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual, and h as the new
  * residual.  h is fp32 and rounded once, into residual_out; y is made of the unrounded h.
+ * mean(h^2) is fp32: past its range a row is zero, and under 2^-111 (|h| about 2e-17) digits are
+ * lost, which shows with an eps as small.
  * Strides in elements; y is dense, in a float type or in the 8-bit format (y its codes,
  * y_scales its scales, both 16-byte aligned).  residual_out may be residual itself, with the
  * same stride, y a dense x of its type; otherwise what is written lies apart from what is read. */
@@ -505,8 +507,9 @@ ecw_status rms_norm(ecw_stream stream, const ecw_rms_norm* norm);
  * j + rotary_dim / 2, or with `neighbours` 2 j and 2 j + 1) is turned by the angle
  * positions[axis_of[j]][row] * frequency j, and multiplied by scale; the dimensions behind
  * stay.  freqs: frequencies as fractions of a turn per position, in 2^-64, modulo a turn.
- * q_out and k_out may be q and k, with the same strides.  The sine and cosine are within 2^-23,
- * products fp32, one rounding into the output. */
+ * q_out and k_out may be q and k, with the same strides; otherwise they lie apart from what is
+ * read.  An angle is within 2^-33 + |position| 2^-65 of a turn, its sine and cosine within
+ * 2^-23, products fp32, one rounding into the output. */
 typedef struct {
   const void *q, *k;             /* [rows][heads][head_dim], strides of rows and heads in elements */
   void *q_out, *k_out;
