@@ -7,7 +7,7 @@ namespace ecw {
 // silu(g) = g / (1 + e^-g).  Below -88.73 e^-g passes fp32's range and the gate is zero.  e^-g is
 // 2^-t times e^(t ln 2 - g) with t the rounded product g log2(e): what t lost, times ln 2, is
 // small, so the second factor is one plus that.  With the library's exponential the vector
-// instructions took as long as the memory (2003 x 14336 bf16 36.4 us).  The instruction gives
+// instructions took as long as the memory (2003 x 14336 bf16 4.0 us more).  The instruction gives
 // zero for reciprocals under 2^-126, so it takes a quarter of 1 + e^-g, and g a quarter too.
 __device__ __forceinline__ float silu(float g) {
   const float h = __builtin_amdgcn_fmed3f(g, -126.f, 126.f), t = h * 1.44269502f;
@@ -17,8 +17,8 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // One lane per 8 elements, 16 lanes per block, so that a block's maximum needs no more than
-// its row of lanes.  Bound by memory (14336 x 4096 bf16 34.0 us, 5.2 TB/s; 2003 x 14336 bf16
-// with a gate 32.4 us, 4.4 TB/s; one row of 14336 2.5 us).
+// its row of lanes.  Bound by memory (14336 x 4096 bf16 32.3 us, 5.5 TB/s; 2003 x 14336 bf16
+// with a gate 30.5 us, 4.7 TB/s; one row of 14336 2.4 us).
 template <int DT, bool GATED>
 __global__ void __launch_bounds__(256) k_fp8_quantise(const void* __restrict__ x, int64_t x_stride,
                                                       const void* __restrict__ gate, int64_t gate_stride, uint32_t rows,
